@@ -1,0 +1,462 @@
+"""The router, its balance loss, MXFP4 quantisation and the MXFP4 products as measured cases.
+
+Each case is one pass through one operator in two forms: the plain form in elementary torch operations (`own` false) and
+the framework's own call (`own` true). `exact` gives the same outputs from the definitions in 64 bits.
+
+Definitions:
+  router   ids = the k largest logits of a row (ties: lowest index; a logit of -inf is an expert that is not available;
+           -1 where fewer than k are), lse = log sum exp of the row, w = softmax over the k selected logits (renormalised)
+           or the softmax of the whole row at the selected ones. A masked row has ids -1, w 0, lse -inf.
+  balance  loss = coefficient * E * sum_e f_e P_e with f_e the share of the valid routes that go to expert e and P_e the
+           mean of the softmax over the valid rows; the gradient takes f_e as a constant.
+  mxfp4    blocks of 32 along the last axis: e = ceil(log2(amax / 6)), at least -127; scale byte e + 127; elements are
+           E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6), x / 2^e rounded to nearest, ties to the even code.
+  linear   y[t][n] = sum_k X[t][k] W[n][k], both operands MXFP4.
+  experts  y_t = sum_j w_tj W2_e q(silu(G) * U), [G | U] = W1_e q(x_t), q the MXFP4 rounding.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def listed():
+    return [
+        # one decode step of 16 streams: the router alone, latency counts
+        dict(name="router_decode_t16", op="router", tokens=16, experts=96, top_k=8, dtype="bf16", renormalize=True,
+             masked=0.0, train=False),
+        # a prompt chunk with padded rows, softmax weights as they are, half precision logits, odd row count
+        dict(name="router_prompt_t2047", op="router", tokens=2047, experts=128, top_k=10, dtype="f16", renormalize=False,
+             masked=0.1, train=False),
+        # a training step over many tokens: selection and the gradient of the logits
+        dict(name="router_train_t16384", op="router", tokens=16384, experts=256, top_k=8, dtype="f32", renormalize=True,
+             masked=0.0, train=True),
+        # the balance loss of one prompt-sized micro-batch, with its gradient
+        dict(name="balance_t2048", op="balance", tokens=2048, experts=96, top_k=8, dtype="f32", masked=0.0),
+        # the balance loss of a large padded batch, bf16 logits
+        dict(name="balance_t32768", op="balance", tokens=32768, experts=256, top_k=8, dtype="bf16", masked=0.25),
+        # the activations of one decode step: quantised and read back
+        dict(name="quantize_decode_16x1024", op="quantize", rows=16, cols=1024, dtype="bf16"),
+        # a layer's expert weights quantised once at load: the largest tensor
+        dict(name="quantize_weights_65536x1024", op="quantize", rows=65536, cols=1024, dtype="f32"),
+        # a single token through a square projection: bound by the weights' bytes
+        dict(name="linear_t1_4096x4096", op="linear", tokens=1, k=4096, n=4096, out="f32"),
+        # an odd prompt through an odd width
+        dict(name="linear_t37_2560x1111", op="linear", tokens=37, k=2560, n=1111, out="bf16"),
+        # a large prompt: bound by the matrix cores
+        dict(name="linear_t4096_4096x4096", op="linear", tokens=4096, k=4096, n=4096, out="bf16"),
+        # one decode step of 16 streams through the experts: bound by the touched experts' bytes
+        dict(name="experts_decode_t16", op="experts", tokens=16, hidden=1024, inter=512, experts=96, top_k=8,
+             routing="uniform", masked=0.0),
+        # a prompt through the experts with uneven popularity
+        dict(name="experts_prefill_t2048", op="experts", tokens=2048, hidden=1024, inter=512, experts=96, top_k=8,
+             routing="zipf", masked=0.0),
+    ]
+
+
+def _spread(rng, lo, hi):
+    """A whole number of [lo, hi], even over its logarithm."""
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["router", "balance", "quantize", "linear", "experts"])
+    if op in ("router", "balance"):
+        experts = _spread(rng, 8, 512)
+        top_k = min(experts, _spread(rng, 1, 16))
+        tokens = _spread(rng, 1, min(32768, (16384 if op == "router" else 32768) * 256 // experts))
+        # the balance loss's gradient is about coefficient / (tokens * experts): below half precision's normal numbers
+        dtype = rng.choice(["f32", "bf16", "f16"] if op == "router" else ["f32", "bf16"])
+        c = dict(op=op, tokens=tokens, experts=experts, top_k=top_k, dtype=dtype, masked=rng.choice([0.0, 0.0, 0.2]))
+        if op == "router":
+            c.update(renormalize=rng.random() < 0.5, train=rng.random() < 0.5)
+        return c
+    if op == "quantize":
+        cols = 32 * _spread(rng, 1, 256)
+        return dict(op=op, rows=_spread(rng, 1, min(65536, 65536 * 1024 // cols)), cols=cols,
+                    dtype=rng.choice(["f32", "bf16", "f16"]))
+    if op == "linear":
+        k, n = 32 * _spread(rng, 4, 128), _spread(rng, 64, 4096)
+        return dict(op=op, tokens=_spread(rng, 1, 4096), k=k, n=n, out=rng.choice(["f32", "bf16"]))
+    hidden, inter = 32 * _spread(rng, 8, 64), 32 * _spread(rng, 4, 24)
+    experts = _spread(rng, 8, 96)
+    top_k = min(experts, _spread(rng, 1, 8))
+    tokens = _spread(rng, 1, max(1, min(2048, 2048 * 8 * 1024 * 512 // (top_k * hidden * inter))))
+    return dict(op=op, tokens=tokens, hidden=hidden, inter=inter, experts=experts, top_k=top_k,
+                routing=rng.choice(["uniform", "zipf"]), masked=rng.choice([0.0, 0.1]))
+
+
+# ---------------------------------------------------------------- plain forms
+
+def _scale_exponent(amax):
+    """ceil(log2(amax / 6)), at least -127: amax = m * 2^x with m in [0.5, 1), and 6 = 0.75 * 2^3."""
+    m, x = torch.frexp(amax)
+    return torch.where(amax > 0, x - 3 + (m > 0.75).to(x.dtype), torch.full_like(x, -127)).clamp(min=-127)
+
+
+def _power(e):
+    """2^e as fp32 for whole e of [-127, 127], from its bits (2^-127 is a subnormal number)."""
+    e = e.to(torch.int32)
+    return torch.where(e < -126, torch.full_like(e, 1 << 22), (e + 127) << 23).view(torch.float32)
+
+
+def _codes_of(x):
+    """fp32 [..., K] -> (element codes uint8 [..., K], scale bytes uint8 [..., K / 32])."""
+    b = x.reshape(*x.shape[:-1], -1, 32)
+    e = _scale_exponent(b.abs().amax(-1))
+    v = b * _power(-e).unsqueeze(-1)
+    m = v.abs()
+    code = (m > 0.25).to(torch.uint8) + (m >= 0.75).to(torch.uint8) + (m > 1.25).to(torch.uint8)
+    code = code + (m >= 1.75).to(torch.uint8) + (m > 2.5).to(torch.uint8) + (m >= 3.5).to(torch.uint8)
+    code = code + (m > 5.0).to(torch.uint8) + 8 * (v < 0).to(torch.uint8)
+    return code.reshape(x.shape), (e + 127).to(torch.uint8)
+
+
+def _pack(code):
+    c = code.reshape(*code.shape[:-1], -1, 2)
+    return (c[..., 0] | (c[..., 1] << 4)).contiguous()
+
+
+def _values_of(code, scales):
+    """fp32 values of element codes [..., K] and scale bytes [..., K / 32]."""
+    table = torch.tensor(E2M1 + tuple(-v for v in E2M1), dtype=torch.float32, device=code.device)
+    v = table[code.to(torch.int32)].reshape(*code.shape[:-1], -1, 32)
+    return (v * _power(scales.to(torch.int32) - 127).unsqueeze(-1)).reshape(code.shape)
+
+
+def _unpack(packed):
+    return torch.stack([packed & 15, packed >> 4], dim=-1).reshape(*packed.shape[:-1], -1)
+
+
+def _rounded(x):
+    return _values_of(*_codes_of(x))
+
+
+def _lse(l):
+    """log sum exp of the rows; -inf for a row of -inf."""
+    m = l.amax(-1)
+    m = torch.where(torch.isinf(m), torch.zeros_like(m), m)
+    return m + torch.log(torch.exp(l - m.unsqueeze(-1)).sum(-1))
+
+
+def _masked_logits(state):
+    l = state["logits"].to(torch.float32)
+    if state["mask"] is not None:
+        l = l.masked_fill(~state["mask"].unsqueeze(-1), -math.inf)
+    return l
+
+
+def _probabilities(l, lse):
+    return torch.exp(l - torch.where(torch.isinf(lse), torch.zeros_like(lse), lse).unsqueeze(-1))
+
+
+def _router(state):
+    k, l = state["top_k"], _masked_logits(state)
+    val, ids = torch.sort(l, dim=-1, descending=True, stable=True)
+    val, ids = val[:, :k], ids[:, :k]
+    there = val > -math.inf
+    lse = _lse(l)
+    base = _lse(val) if state["renormalize"] else lse
+    w = _probabilities(val, base)
+    out = dict(ids=torch.where(there, ids, torch.full_like(ids, -1)), w=w, lse=lse)
+    if state["train"]:
+        g = w * state["dw"]
+        s = g.sum(-1, keepdim=True)
+        if state["renormalize"]:
+            d = torch.zeros_like(l).scatter_(1, ids, g - w * s)
+        else:
+            d = (-s * _probabilities(l, lse)).scatter_add_(1, ids, g)
+        out["dlogits"] = d.to(state["logits"].dtype)
+    return out
+
+
+def _balance(state):
+    l, lse, ids = state["logits"].to(torch.float32), state["lse"], state["ids"]
+    E = l.shape[1]
+    row = (lse > -math.inf).unsqueeze(-1)
+    n = row.sum().clamp(min=1)
+    p = torch.where(row, _probabilities(l, lse), torch.zeros_like(l))
+    counts = torch.zeros(E + 1, dtype=torch.int64, device=l.device)
+    counts = counts.scatter_add_(0, torch.where(ids < 0, E, ids).reshape(-1), torch.ones_like(ids).reshape(-1))[:E]
+    f = counts.to(torch.float32) / counts.sum().clamp(min=1)
+    c = state["coefficient"] * E
+    loss = c * (f * (p.sum(0) / n)).sum()
+    d = state["dloss"] * (c / n) * p * (f - (p * f).sum(-1, keepdim=True))
+    return dict(loss=loss, counts=counts.to(torch.int32), dlogits=d.to(state["logits"].dtype))
+
+
+def _experts(state):
+    """Every expert's tokens in a padded row block, so that the products are batched ones."""
+    x, ids, w, cap, E = state["x"], state["ids"], state["w"], state["cap"], state["experts"]
+    T, k = ids.shape
+    e = ids.reshape(-1)
+    order = torch.sort(torch.where(e < 0, E, e), stable=True)[1]
+    sorted_e = torch.where(e < 0, E, e)[order]
+    first = torch.searchsorted(sorted_e, sorted_e, right=False)
+    place = torch.arange(T * k, device=e.device) - first
+    at = torch.where(sorted_e < E, sorted_e * cap + place, E * cap)
+    xq = _rounded(x.to(torch.float32))
+    a = torch.zeros(E * cap + 1, x.shape[1], dtype=torch.float32, device=x.device)
+    a[at] = xq[order // k]
+    a = a[:-1].reshape(E, cap, -1)
+    w1 = _values_of(_unpack(state["w1"]), state["s1"]).transpose(1, 2).contiguous()
+    z = torch.bmm(a, w1)
+    del w1
+    g, u = z.chunk(2, dim=-1)
+    b = _rounded((g / (1.0 + torch.exp(-g)) * u).contiguous())
+    w2 = _values_of(_unpack(state["w2"]), state["s2"]).transpose(1, 2).contiguous()
+    v = torch.bmm(b, w2).reshape(E * cap, -1)
+    slot = torch.empty_like(at).scatter_(0, order, at).reshape(T, k)
+    there = (slot < E * cap).unsqueeze(-1)
+    rows = torch.where(there, v[slot.clamp(max=E * cap - 1)], torch.zeros((), device=v.device))
+    return (rows * w.unsqueeze(-1)).sum(1).to(torch.bfloat16)
+
+
+# ---------------------------------------------------------------- inputs
+
+def _generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(int(seed))
+    return g
+
+
+def _normal(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda", dtype=torch.float32)
+
+
+def _logits(g, case):
+    """Router logits: a popularity of each expert and a token's own part, some experts not available to some tokens."""
+    T, E = case["tokens"], case["experts"]
+    l = _normal(g, T, E) * 1.5 + _normal(g, E)
+    l = l.masked_fill(torch.rand(T, E, generator=g, device="cuda") < 0.02, -math.inf)
+    mask = None
+    if case["masked"]:
+        mask = torch.rand(T, generator=g, device="cuda") >= case["masked"]
+        l = l.masked_fill(~mask.unsqueeze(-1) & (torch.rand(T, E, generator=g, device="cuda") < 0.1), math.nan)
+    return l.to(DTYPES[case["dtype"]]), mask
+
+
+def _quantised(g, *shape):
+    code, scales = _codes_of(_normal(g, *shape) * (1.0 / math.sqrt(shape[-1])))
+    return _pack(code), scales.contiguous()
+
+
+def _inputs(case, seed):
+    g, op = _generator(seed), case["op"]
+    if op == "router":
+        l, mask = _logits(g, case)
+        return dict(op=op, logits=l, mask=mask, top_k=case["top_k"], renormalize=case["renormalize"], train=case["train"],
+                    dw=_normal(g, case["tokens"], case["top_k"]))
+    if op == "balance":
+        l, mask = _logits(g, case)
+        s = dict(op=op, logits=l, mask=mask, top_k=case["top_k"], renormalize=True, train=False)
+        r = _router(s)
+        return dict(op=op, logits=l, lse=r["lse"].contiguous(), ids=r["ids"].contiguous(), coefficient=0.01,
+                    dloss=torch.rand((), generator=g, device="cuda") + 0.5)
+    if op == "quantize":
+        x = _normal(g, case["rows"], case["cols"])
+        x = torch.where(torch.rand(x.shape, generator=g, device="cuda") < 0.01, x * 20.0, x)
+        return dict(op=op, x=x.to(DTYPES[case["dtype"]]))
+    if op == "linear":
+        xq, xs = _quantised(g, case["tokens"], case["k"])
+        wq, ws = _quantised(g, case["n"], case["k"])
+        return dict(op=op, xq=xq, xs=xs, wq=wq, ws=ws, out=DTYPES[case["out"]])
+    T, E, k, H, I = case["tokens"], case["experts"], case["top_k"], case["hidden"], case["inter"]
+    w1, s1 = _quantised(g, E, 2 * I, H)
+    w2, s2 = _quantised(g, E, H, I)
+    x = _normal(g, T, H).to(torch.bfloat16)
+    score = -torch.log(-torch.log(torch.rand(T, E, generator=g, device="cuda").clamp(1e-20, 1 - 1e-7)))
+    if case["routing"] == "zipf":
+        rank = torch.randperm(E, generator=g, device="cuda").to(torch.float32) + 1.0
+        score = score - 1.1 * torch.log(rank)
+    ids = torch.sort(score, dim=1, descending=True)[1][:, :k].contiguous()
+    w = torch.softmax(_normal(g, T, k), dim=1)
+    if case["masked"]:
+        out = torch.rand(T, generator=g, device="cuda") < case["masked"]
+        ids, w = ids.masked_fill(out.unsqueeze(-1), -1), w.masked_fill(out.unsqueeze(-1), 0.0)
+    cap = int(torch.bincount(ids[ids >= 0].reshape(-1), minlength=E).max()) if bool((ids >= 0).any()) else 1
+    return dict(op=op, x=x, ids=ids, w=w, w1=w1, s1=s1, w2=w2, s2=s2, experts=E, cap=max(cap, 1))
+
+
+def prepare(case, seed):
+    s = _inputs(case, seed)
+    if own and case["op"] == "experts":   # the plan, weights and scratch that a program keeps
+        from trellis_quantized_moe_tmoe_amd import mxfp4
+        s["plan"] = mxfp4.ExpertPlan(case["hidden"], case["inter"], case["experts"], case["top_k"],
+                                     max_tokens=case["tokens"], out_dtype=torch.bfloat16)
+        s["weights"] = mxfp4.ExpertWeights(s["w1"], s["s1"], s["w2"], s["s2"])
+        s["scratch"] = s["plan"].alloc_scratch()
+    return s
+
+
+# ---------------------------------------------------------------- one pass
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+def _plain(state):
+    op = state["op"]
+    if op == "router":
+        return _router(state)
+    if op == "balance":
+        return _balance(state)
+    if op == "quantize":
+        code, scales = _codes_of(state["x"].to(torch.float32))
+        return dict(values=_values_of(code, scales).to(state["x"].dtype), scales=scales)
+    if op == "linear":
+        x = _values_of(_unpack(state["xq"]), state["xs"])
+        w = _values_of(_unpack(state["wq"]), state["ws"])
+        return torch.matmul(x, w.t().contiguous()).to(state["out"])
+    return _experts(state)
+
+
+def _own(state):
+    from trellis_quantized_moe_tmoe_amd import mxfp4, router
+    op = state["op"]
+    if op == "router":
+        ids, w, lse = router.topk(state["logits"], state["top_k"], renormalize=state["renormalize"],
+                                  token_mask=state["mask"])
+        out = dict(ids=ids, w=w, lse=lse)
+        if state["train"]:
+            out["dlogits"] = router.backward(state["logits"], lse, ids, w=w, dw=state["dw"],
+                                             renormalize=state["renormalize"])
+        return out
+    if op == "balance":
+        loss, counts = router.balance_loss(state["logits"], state["lse"], state["ids"], state["coefficient"])
+        d = router.backward(state["logits"], state["lse"], state["ids"], counts=counts, dloss=state["dloss"],
+                            coefficient=state["coefficient"])
+        return dict(loss=loss, counts=counts, dlogits=d)
+    if op == "quantize":
+        codes, scales = mxfp4.quantize(state["x"])
+        return dict(values=mxfp4.dequantize(codes, scales, state["x"].dtype), scales=scales)
+    if op == "linear":
+        return mxfp4.linear(state["xq"], state["xs"], state["wq"], state["ws"], out_dtype=state["out"])
+    return state["plan"].forward(state["x"], state["ids"], state["w"], state["weights"], state["scratch"])
+
+
+# ---------------------------------------------------------------- 64 bits
+
+def _exact_router(state):
+    l = state["logits"].double()
+    T, E = l.shape
+    keep = torch.ones(T, dtype=torch.bool, device=l.device) if state["mask"] is None else state["mask"]
+    live = (l > -math.inf) & keep[:, None]
+    top = torch.where(live, l, torch.full_like(l, -1e300)).max(1, keepdim=True).values
+    ex = torch.where(live, torch.exp(l - top), torch.zeros_like(l))
+    total = ex.sum(1, keepdim=True)
+    some = total > 0
+    p = torch.where(some, ex / torch.where(some, total, torch.ones_like(total)), torch.zeros_like(ex))
+    lse = torch.where(some, top + torch.log(torch.where(some, total, torch.ones_like(total))),
+                      torch.full_like(total, -math.inf))[:, 0]
+    return l, live, p, lse
+
+
+def _exact_values(packed, scales):
+    low, high = (packed & 15).long(), (packed >> 4).long()
+    code = torch.empty(*packed.shape[:-1], 2 * packed.shape[-1], dtype=torch.long, device=packed.device)
+    code[..., 0::2], code[..., 1::2] = low, high
+    mag, man = (code >> 1) & 3, code & 1
+    v = torch.where(mag == 0, 0.5 * man.double(), (1 + 0.5 * man.double()) * torch.exp2(mag.double() - 1))
+    v = torch.where(code >= 8, -v, v)
+    return v * torch.exp2(scales.double() - 127).repeat_interleave(32, dim=-1)
+
+
+def _exact_rounded(x):
+    """Values of the MXFP4 rounding of float64 x [rows][cols], by the nearest of the eight magnitudes."""
+    grid = torch.tensor(E2M1, dtype=torch.float64, device=x.device)
+    b = x.reshape(-1, 32)
+    amax = b.abs().max(1).values
+    e = torch.where(amax > 0, torch.ceil(torch.log2(torch.where(amax > 0, amax, torch.ones_like(amax)) / 6.0)),
+                    torch.full_like(amax, -127.0))
+    e = torch.where((amax > 0) & (amax <= 6.0 * torch.exp2(e - 1)), e - 1, e)   # log2's own rounding
+    e = torch.where((amax > 0) & (amax > 6.0 * torch.exp2(e)), e + 1, e).clamp(min=-127.0)
+    m = (b / torch.exp2(e)[:, None]).abs()
+    at = torch.bucketize(m, (grid[1:] + grid[:-1]) / 2, right=False)            # border -> lower code
+    border = torch.zeros_like(m, dtype=torch.bool)
+    for lower in (1, 3, 5):                                                      # borders whose upper code is even
+        border |= m == (grid[lower] + grid[lower + 1]) / 2
+    at = torch.where(border, at + 1, at)
+    v = grid[at] * torch.exp2(e)[:, None]
+    return torch.where(b < 0, -v, v).reshape(x.shape), (e + 127).to(torch.uint8).reshape(*x.shape[:-1], -1)
+
+
+def exact(case, seed):
+    s, op = _inputs(case, seed), case["op"]
+    if op == "router":
+        l, live, p, lse = _exact_router(s)
+        score = torch.where(live, l, torch.full_like(l, -math.inf)).cpu().numpy()
+        order = torch.from_numpy(np.argsort(-score, axis=1, kind="stable")[:, :case["top_k"]].copy()).cuda()
+        there = torch.gather(live, 1, order)
+        w = torch.where(there, torch.gather(p, 1, order), torch.zeros((), dtype=torch.float64, device="cuda"))
+        if case["renormalize"]:
+            t = w.sum(1, keepdim=True)
+            w = torch.where(t > 0, w / torch.where(t > 0, t, torch.ones_like(t)), torch.zeros_like(w))
+        out = dict(ids=None, w=w, lse=lse)
+        if case["train"]:
+            dw = s["dw"].double()
+            dot = (w * dw).sum(1, keepdim=True)
+            if case["renormalize"]:
+                d = torch.zeros_like(p)
+            else:
+                d = -dot * p
+            share = w * (dw - dot) if case["renormalize"] else w * dw
+            out["dlogits"] = d.scatter_add_(1, order, torch.where(there, share, torch.zeros_like(share)))
+        return out
+    if op == "balance":
+        l, ids, E = s["logits"].double(), s["ids"], case["experts"]
+        row = s["lse"] > -math.inf
+        n = max(1, int(row.sum()))
+        l = torch.where(row[:, None], l, torch.zeros_like(l))
+        ex = torch.exp(l - l.max(1, keepdim=True).values)
+        p = ex / ex.sum(1, keepdim=True) * row[:, None]
+        c = torch.bincount(ids[ids >= 0].reshape(-1), minlength=E).double()
+        f = c / max(1.0, float(c.sum()))
+        scale = s["coefficient"] * E / n
+        d = float(s["dloss"]) * scale * (p * f - p * (p @ f)[:, None])
+        return dict(loss=scale * (p @ f).sum(), counts=None, dlogits=d)
+    if op == "quantize":
+        return dict(values=_exact_rounded(s["x"].double())[0], scales=None)
+    if op == "linear":
+        x, w = _exact_values(s["xq"], s["xs"]), _exact_values(s["wq"], s["ws"])
+        return torch.matmul(x, w.t().contiguous())
+    xq = _exact_rounded(s["x"].double())[0]
+    y = torch.zeros(case["tokens"], case["hidden"], dtype=torch.float64, device="cuda")
+    for e in range(case["experts"]):
+        t, j = torch.nonzero(s["ids"] == e, as_tuple=True)
+        if not len(t):
+            continue
+        z = torch.matmul(xq[t], _exact_values(s["w1"][e], s["s1"][e]).t().contiguous())
+        g, u = z[:, :case["inter"]], z[:, case["inter"]:]
+        b = _exact_rounded((g * torch.sigmoid(g) * u).contiguous())[0]
+        v = torch.matmul(b, _exact_values(s["w2"][e], s["s2"][e]).t().contiguous())
+        y.index_add_(0, t, v * s["w"].double()[t, j][:, None])
+    return y
+
+
+# ---------------------------------------------------------------- work
+
+def work(case):
+    op = case["op"]
+    size = {"f32": 4, "bf16": 2, "f16": 2}
+    if op == "router":
+        T, E, k, s = case["tokens"], case["experts"], case["top_k"], size[case["dtype"]]
+        train = T * (E * s + 4 * k) if case["train"] else 0
+        return dict(bytes=T * (E * s + 12 * k + 4) + train, flops=4 * T * E * (2 if case["train"] else 1))
+    if op == "balance":
+        T, E, k, s = case["tokens"], case["experts"], case["top_k"], size[case["dtype"]]
+        return dict(bytes=T * (2 * E * s + 8 * k + 4), flops=8 * T * E)
+    if op == "quantize":
+        n = case["rows"] * case["cols"]
+        return dict(bytes=n * (2 * size[case["dtype"]] + 17 / 32), flops=4 * n)
+    if op == "linear":
+        T, K, N = case["tokens"], case["k"], case["n"]
+        return dict(bytes=(T + N) * K * 17 / 32 + T * N * size[case["out"]], flops=2 * T * K * N)
+    T, H, I, E, k = case["tokens"], case["hidden"], case["inter"], case["experts"], case["top_k"]
+    touched = E * (1 - (1 - k / E) ** T) if k < E else E
+    return dict(bytes=touched * 3 * H * I * 17 / 32 + T * H * 4 + 12 * T * k, flops=6 * T * k * H * I)
