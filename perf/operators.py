@@ -328,9 +328,8 @@ def _own(state):
                                              renormalize=state["renormalize"])
         return out
     if op == "balance":
-        loss, counts = router.balance_loss(state["logits"], state["lse"], state["ids"], state["coefficient"])
-        d = router.backward(state["logits"], state["lse"], state["ids"], counts=counts, dloss=state["dloss"],
-                            coefficient=state["coefficient"])
+        loss, counts, slope = router.balance_loss(state["logits"], state["lse"], state["ids"], state["coefficient"])
+        d = router.backward(state["logits"], state["lse"], state["ids"], slope=slope, dloss=state["dloss"])
         return dict(loss=loss, counts=counts, dlogits=d)
     if op == "quantize":
         codes, scales = mxfp4.quantize(state["x"])
