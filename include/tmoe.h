@@ -236,6 +236,60 @@ tmoe_status tmoe_linear_w4a16(tmoe_linear_plan_t plan, const void *x_bf16, int32
                               const tmoe_linear_weights *weights, float *y, void *scratch,
                               size_t scratch_bytes, void *stream);
 
+/* ---- router: the ids and weights that the forwards take, and the loss that balances them ----
+ * Rows of E logits l, one per token; a logit of -inf is an expert that is not available to the token.
+ *   lse_t = log sum_e exp(l_te); -inf for a row left out by the mask or with no available expert
+ *   ids   = the top_k largest logits, largest first, ties to the lowest expert; -1 (a dropped route)
+ *           where fewer than top_k experts are available
+ *   w_j   = exp(l_j) / sum over the selected logits (renormalize = 1) or over all E logits (0);
+ *           0 where the id is -1
+ * A NaN or +inf logit in a row that is not left out makes the row's weights and lse NaN; its ids stay
+ * valid (NaN is never selected). Rows that are left out may hold anything. Softmax statistics and sums
+ * are held in fp32 or more for every logits type. */
+enum { TMOE_F32 = 0, TMOE_BF16 = 1, TMOE_F16 = 2 };      /* element types of the calls below */
+
+typedef struct {
+  int32_t num_experts;         /* E: 1..512                                                      */
+  int32_t top_k;               /* k: 1..32, at most E                                            */
+  int32_t logits_dtype;        /* TMOE_F32, TMOE_BF16 or TMOE_F16 (also the type of dlogits)     */
+  int32_t ids_dtype;           /* TMOE_IDS_I32 or TMOE_IDS_I64                                   */
+  int32_t renormalize;         /* 0 or 1                                                         */
+} tmoe_router_config;
+
+/* logits: [T] rows of E values, logits_stride elements from row to row (>= E); token_mask: [T] bytes, 0
+ * leaves the row out, or null; ids: [T][k]; w: fp32 [T][k]; lse: fp32 [T]. T <= 2^24; T = 0 launches
+ * nothing. One launch. Errors as for the forwards (logits aligned to their element size). */
+tmoe_status tmoe_router_topk(const tmoe_router_config *cfg, const void *logits, int64_t logits_stride,
+                             const uint8_t *token_mask, int32_t T, void *ids, float *w, float *lse,
+                             void *stream);
+
+/* Balance loss. n = rows with lse > -inf, c_e = ids equal to e, f_e = c_e / sum c, P_e = the mean of
+ * exp(l_te - lse_t) over those n rows:
+ *   loss = coefficient * E * sum_e f_e P_e          (coefficient for a uniform router; 0 if n = 0)
+ * counts: int32 [E], c_e; slope: fp32 [E], dloss/dp_te = coefficient * E * f_e / n (f taken as a
+ * constant), which tmoe_router_backward reads. ids and lse as tmoe_router_topk writes them (ids outside
+ * [0, E) are not counted). Sums run in a fixed order: repeated calls give identical bits. Scratch:
+ * tmoe_balance_loss_scratch bytes, 16-byte aligned, under the scratch rules above. Two launches; T = 0
+ * writes zeros (one launch). */
+tmoe_status tmoe_balance_loss_scratch(const tmoe_router_config *cfg, int32_t T, size_t *scratch_bytes);
+tmoe_status tmoe_balance_loss(const tmoe_router_config *cfg, const void *logits, int64_t logits_stride,
+                              const float *lse, const void *ids, int32_t T, float coefficient, float *loss,
+                              int32_t *counts, float *slope, void *scratch, size_t scratch_bytes, void *stream);
+
+/* Gradient of the logits, dlogits [T][E] (contiguous, of the logits' type, fully overwritten):
+ *   from the weights (w and dw, fp32 [T][k], both given): renormalize = 1
+ *       dl_e = w_j (dw_j - sum_i w_i dw_i) where e = ids_j, 0 elsewhere;
+ *     renormalize = 0  dl_e = [e = ids_j] w_j dw_j - p_e sum_i w_i dw_i;
+ *   from the balance loss (slope and dloss, fp32 [E] and [1], both given):
+ *       dl_e = dloss p_e (slope_e - sum p slope).
+ * Either pair may be null; with both the parts add up in fp32 before the one rounding. Rows with
+ * lse = -inf and routes with an id outside [0, E) get nothing, whatever w, dw and the logits hold there.
+ * The ids of a row are distinct, as tmoe_router_topk writes them. One launch; T = 0 launches nothing. */
+tmoe_status tmoe_router_backward(const tmoe_router_config *cfg, const void *logits, int64_t logits_stride,
+                                 const float *lse, const void *ids, const float *w, const float *dw,
+                                 const float *slope, const float *dloss, int32_t T, void *dlogits,
+                                 void *stream);
+
 /* ---- test hooks: expose single steps so their bit-exactness can be graded ---- */
 
 /* Decode expert `expert`'s FC1 (matrix 0, H x 2I) or FC2 (matrix 1, I x H) with the same device

@@ -1,6 +1,7 @@
 """Trellis-quantized routed MoE layer for MI355X (gfx950): HIP kernels behind a C ABI.
 
 Import `trellis_quantized_moe_tmoe_amd.layer` for the torch-facing wrapper (it loads libtmoe.so and
-fails if the library is not built) and `trellis_quantized_moe_tmoe_amd.workloads` for seeded inputs.
+fails if the library is not built), `trellis_quantized_moe_tmoe_amd.router` for the ids and weights it takes
+(top-k, balance loss, gradients) and `trellis_quantized_moe_tmoe_amd.workloads` for seeded inputs.
 """
-__all__ = ["layer", "native", "workloads"]
+__all__ = ["layer", "native", "router", "workloads"]

@@ -47,6 +47,15 @@ def _same_device(named) -> None:
         raise ValueError(f"tensors must be on a GPU device, got {dev}")
 
 
+def _launch(device, fn, where: str, *args) -> None:
+    """fn(*args, stream) with `device` current and its current torch stream, raising on an error status."""
+    if device.index == torch.cuda.current_device():
+        check(fn(*args, _stream(device)), where)
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, _stream(device)), where)
+
+
 def _check_scratch(scratch, need: int) -> None:
     if not isinstance(scratch, torch.Tensor) or scratch.dtype != torch.uint8 or scratch.dim() != 1:
         raise ValueError("scratch: expected a 1-D uint8 tensor")

@@ -18,6 +18,7 @@ STATIC_SCRATCH_BYTES = 32 << 20
 ROT_HADAMARD, ROT_IDENTITY = 0, 1
 FC2_DETERMINISTIC, FC2_ATOMIC = 0, 1
 IDS_I32, IDS_I64 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 
 # every symbol declared in include/tmoe.h
 EXPORTS = ["tmoe_plan", "tmoe_plan_destroy", "tmoe_plan_get_info", "tmoe_plan_expert_offset",
@@ -25,7 +26,8 @@ EXPORTS = ["tmoe_plan", "tmoe_plan_destroy", "tmoe_plan_get_info", "tmoe_plan_ex
            "tmoe_forward_stages",
            "tmoe_status_str",
            "tmoe_debug_decode", "tmoe_debug_mxfp8", "tmoe_debug_rotate", "tmoe_debug_get_views",
-           "tmoe_linear_plan", "tmoe_linear_plan_destroy", "tmoe_linear_w4a16"]
+           "tmoe_linear_plan", "tmoe_linear_plan_destroy", "tmoe_linear_w4a16",
+           "tmoe_router_topk", "tmoe_balance_loss_scratch", "tmoe_balance_loss", "tmoe_router_backward"]
 
 
 class Config(ctypes.Structure):
@@ -67,6 +69,11 @@ class LinearWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("payload", "scale", "su", "sv")]
 
 
+class RouterConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+                ("ids_dtype", ctypes.c_int32), ("renormalize", ctypes.c_int32)]
+
+
 class TmoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}")
@@ -105,6 +112,11 @@ def _load():
                                      ctypes.POINTER(SZ)]
     lib.tmoe_linear_plan_destroy.argtypes = [P]
     lib.tmoe_linear_w4a16.argtypes = [P, P, I32, ctypes.POINTER(LinearWeights), P, P, SZ, P]
+    RC, F = ctypes.POINTER(RouterConfig), ctypes.c_float
+    lib.tmoe_router_topk.argtypes = [RC, P, I64, P, I32, P, P, P, P]
+    lib.tmoe_balance_loss_scratch.argtypes = [RC, I32, ctypes.POINTER(SZ)]
+    lib.tmoe_balance_loss.argtypes = [RC, P, I64, P, P, I32, F, P, P, P, P, SZ, P]
+    lib.tmoe_router_backward.argtypes = [RC, P, I64, P, P, P, P, P, P, I32, P, P]
     for name in EXPORTS:
         if name != "tmoe_status_str":
             getattr(lib, name).restype = I32
