@@ -290,6 +290,63 @@ tmoe_status tmoe_router_backward(const tmoe_router_config *cfg, const void *logi
                                  const float *slope, const float *dloss, int32_t T, void *dlogits,
                                  void *stream);
 
+/* ---- MXFP4: quantisation, the dense product and the expert layer ----
+ * Rows of K values (K a multiple of 32) in blocks of 32 neighbours: E2M1 codes, two in a byte (element 2i
+ * in the low nibble of byte i), codes [rows][K/2], and one E8M0 byte per block, scales [rows][K/32]; the
+ * value is code * 2^(byte - 127), 255 = NaN (OCP Microscaling Formats, version 1.0). The scale is the
+ * smallest power of two (at least 2^-127) with amax / 2^e <= 6, so nothing saturates (the layer's MXFP8
+ * rule with E2M1's largest value); elements round to nearest, ties to the even code. A block with an
+ * infinity or a NaN gets scale 255 and codes 0. */
+
+/* x: rows x cols values of `dtype` (TMOE_F32, TMOE_BF16, TMOE_F16), contiguous, 16-byte aligned; codes 16-byte
+ * aligned. rows * cols < 2^40; rows = 0 launches nothing. One launch. */
+tmoe_status tmoe_mxfp4_quantize(const void *x, int32_t dtype, int64_t rows, int32_t cols, uint8_t *codes,
+                                uint8_t *scales, void *stream);
+/* The values of codes and scales in `dtype`, rounded once (TMOE_BF16 and TMOE_F32 hold them exactly unless
+ * they leave that type's range). */
+tmoe_status tmoe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols,
+                                  int32_t dtype, void *x, void *stream);
+
+/* y[t][n] = sum_k X[t][k] W[n][k], X [T][K] and W [N][K] MXFP4, y [T][N] of y_dtype (TMOE_F32 or TMOE_BF16),
+ * fully overwritten. Products are exact, sums fp32. K: a multiple of 32, 32..65536; N: 1..65536;
+ * T <= 2^20; T = 0 launches nothing. Codes and y 16-byte aligned. One launch; deterministic. */
+tmoe_status tmoe_linear_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, int32_t T, const uint8_t *w_codes,
+                              const uint8_t *w_scales, int32_t K, int32_t N, int32_t y_dtype, void *y,
+                              void *stream);
+
+/* The routed expert layer with MXFP4 weights and activations (q = the rounding above):
+ *   [G | U] = W1_e q(x_t);  b = q(silu(G) * U);  y_t = sum over j ascending of w[t][j] * (W2_e b)
+ * for e = ids[t][j]; ids outside [0, E) are dropped routes. No rotations, signs or channel scales. */
+typedef struct {
+  int32_t hidden;              /* H: multiple of 32, 32..8192                                   */
+  int32_t inter;               /* I: multiple of 32, 32..8192                                   */
+  int32_t num_experts;         /* E: 1..512                                                     */
+  int32_t top_k;               /* k: 1..32                                                      */
+  int32_t max_tokens;          /* capacity T_max >= 1; T*k <= 2^22                              */
+  int32_t ids_dtype;           /* TMOE_IDS_I32 or TMOE_IDS_I64                                   */
+  int32_t y_dtype;             /* TMOE_F32 or TMOE_BF16                                          */
+} tmoe_mxfp4_config;
+
+typedef struct tmoe_mxfp4_plan_s *tmoe_mxfp4_plan_t;   /* opaque, host-only, immutable */
+
+typedef struct {                 /* device pointers, read only; codes 16-byte aligned */
+  const uint8_t *w1;             /* [E][2I][H/2]  gate rows first, then up rows                  */
+  const uint8_t *s1;             /* [E][2I][H/32]                                                */
+  const uint8_t *w2;             /* [E][H][I/2]                                                  */
+  const uint8_t *s2;             /* [E][H][I/32]                                                 */
+} tmoe_mxfp4_weights;
+
+/* Validate and plan (host only). scratch_bytes may be NULL. Errors: INVALID_ARG, UNSUPPORTED. */
+tmoe_status tmoe_mxfp4_plan(const tmoe_mxfp4_config *cfg, tmoe_mxfp4_plan_t *out, size_t *scratch_bytes);
+tmoe_status tmoe_mxfp4_plan_destroy(tmoe_mxfp4_plan_t plan);
+
+/* x: bf16 [T][H]; topk_ids [T][k]; topk_w: fp32 [T][k]; y: [T][H] of the plan's y_dtype, fully
+ * overwritten (x, y 16-byte aligned). Arena, stream, capture and error rules as for the forwards above.
+ * Deterministic: repeated calls give identical bits. */
+tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t plan, const void *x_bf16, const void *topk_ids,
+                               const float *topk_w, int32_t T, const tmoe_mxfp4_weights *weights, void *y,
+                               void *scratch, size_t scratch_bytes, void *stream);
+
 /* ---- test hooks: expose single steps so their bit-exactness can be graded ---- */
 
 /* Decode expert `expert`'s FC1 (matrix 0, H x 2I) or FC2 (matrix 1, I x H) with the same device

@@ -11,10 +11,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(HERE, "libtmoe.so")
-SOURCES = ["k_route_map.hip", "k_rowops.hip", "k_trellis_gemm.hip", "k_small_arm.hip", "k_router.hip", "tmoe_host.cpp",
-           "tmoe_router_host.cpp"]
+SOURCES = ["k_route_map.hip", "k_rowops.hip", "k_trellis_gemm.hip", "k_small_arm.hip", "k_router.hip", "k_mxfp4_quant.hip",
+           "k_mxfp4_gemm.hip", "tmoe_host.cpp", "tmoe_router_host.cpp", "tmoe_mxfp4_host.cpp"]
 HEADERS = ["tmoe_device.hpp", "tmoe_hadamard.hpp", "tmoe_internal.hpp", "tmoe_rowbody.hpp", "tmoe_routemap.hpp",
-           "tmoe_router.hpp"]
+           "tmoe_router.hpp", "tmoe_mxfp4.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

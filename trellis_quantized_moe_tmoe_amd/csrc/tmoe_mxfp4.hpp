@@ -1,0 +1,91 @@
+// tmoe_mxfp4.hpp -- MXFP4 pieces: the block format on the device, launch arguments and launchers.
+//
+// MXFP4 (OCP Microscaling Formats, version 1.0): blocks of 32 values along the contraction axis, E2M1
+// elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one E8M0 scale byte (2^(byte - 127),
+// 255 = NaN) per block. Element 2i of a row is the low nibble of byte i.
+#pragma once
+#include "tmoe_device.hpp"
+
+namespace tmoe {
+
+// Scale byte of a block with the largest magnitude amax, given as the bits of |amax|: the smallest
+// power of two 2^e with amax / 2^e <= 6 (so nothing saturates), e >= -127. amax = 2^x * 1.m lies in
+// (6 * 2^(e-1), 6 * 2^e] with 6 = 1.5 * 2^2, so e = x - 2, plus 1 where 1.m > 1.5; subnormal amax
+// gives -127. An infinity or a NaN in the block gives 255.
+__device__ __forceinline__ uint32_t mxfp4_scale_byte(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return 255u;
+  const int byte = static_cast<int>(amax_bits >> 23) - 2 + ((amax_bits & 0x7fffffu) > 0x400000u ? 1 : 0);
+  return static_cast<uint32_t>(byte > 0 ? byte : 0);
+}
+
+// 2^-(byte - 127), exact for every byte below 255; 0 for 255, so that block's codes come out as zeros
+// of either sign or (0 * inf) are replaced by the caller.
+__device__ __forceinline__ float mxfp4_inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// 2^(byte - 127); NaN for 255.
+__device__ __forceinline__ float mxfp4_scale(uint32_t byte) {
+  if (byte == 255u) return __uint_as_float(0x7fc00000u);
+  return __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+}
+
+// Eight values already divided by their block's scale -> eight codes, round to nearest even.
+__device__ __forceinline__ uint32_t mxfp4_codes8(const float (&v)[8]) {
+  uint32_t r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], 1.0f, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], 1.0f, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4], v[5], 1.0f, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6], v[7], 1.0f, 3);
+}
+
+struct Mxfp4QuantArgs {
+  const void* x;             // [rows][cols], contiguous
+  long long groups;          // rows * cols / 8
+  uint8_t* codes;            // [rows][cols / 2]
+  uint8_t* scales;           // [rows][cols / 32]
+};
+
+struct Mxfp4DequantArgs {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  long long groups;
+  void* x;
+};
+
+// out[row][n] = sum_k X[row][k] W[n][k] over MXFP4 rows of K values. Dense: row tiles of the T rows.
+// Grouped: tile i of the list holds rows [y, y + z) (slots) of expert x; X row of a slot:
+// sorted[slot] / top_k (first product) or the slot itself (second).
+struct Mxfp4GemmArgs {
+  const uint8_t* xq;         // [rows][K / 2]
+  const uint8_t* xs;         // [rows][K / 32]
+  const uint8_t* wq;         // [N][K / 2] (times experts)
+  const uint8_t* ws;         // [N][K / 32]
+  int K, N;
+  int rows;                  // dense: T
+  const int4* gtiles;
+  const int32_t* num_gtiles;
+  int max_gtiles;
+  const int32_t* sorted;     // first product: slot -> route
+  int top_k;
+  void* y;                   // dense: [T][N] fp32 or bf16; second product: fp32 [slots][N]
+  uint8_t* bq;               // first product: [slots][N / 4] codes of silu(gate) * up (N = 2I)
+  uint8_t* bs;               // [slots][N / 64]
+};
+
+struct Mxfp4CombineArgs {
+  const float* v;            // [slots][H]
+  const int32_t* route_slot; // [T][k], -1 = dropped
+  const float* w;            // [T][k]
+  int tokens, top_k, H;
+  void* y;                   // [T][H] fp32 or bf16
+};
+
+// dtype: TMOE_F32, TMOE_BF16 or TMOE_F16
+void launch_mxfp4_quantize(const Mxfp4QuantArgs& a, int dtype, hipStream_t s);
+void launch_mxfp4_dequantize(const Mxfp4DequantArgs& a, int dtype, hipStream_t s);
+void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s);
+// tile_rows: rows of the tile list's tiles, as mxfp4_tile_rows chose them
+void launch_mxfp4_fc1(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s);
+void launch_mxfp4_fc2(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s);
+void launch_mxfp4_combine(const Mxfp4CombineArgs& a, int y_dtype, hipStream_t s);
+int mxfp4_tile_rows(long long routes, int experts);
+
+}  // namespace tmoe

@@ -1,0 +1,161 @@
+"""MXFP4 (E2M1 elements, one E8M0 scale per 32): quantisation, the dense product and the expert layer.
+
+Thin wrappers of tmoe_mxfp4_quantize, tmoe_mxfp4_dequantize, tmoe_linear_mxfp4 and tmoe_forward_mxfp4
+(include/tmoe.h holds the format and the formulas). Codes and scales are uint8 tensors [..., K/2] and
+[..., K/32]; weights are rows of output features, quantised along their input features:
+`ExpertWeights(*quantize(w1), *quantize(w2))` with w1 [E, 2I, H] (gate rows first) and w2 [E, H, I]."""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import native
+from .layer import _BITS16, _check_scratch, _launch, _require, _same_device
+from .native import check, lib
+
+_DTYPES = {torch.float32: native.F32, torch.bfloat16: native.BF16, torch.float16: native.F16}
+_OUT = {torch.float32: native.F32, torch.bfloat16: native.BF16}
+
+
+def _out_dtype(dtype) -> int:
+    if dtype not in _OUT:
+        raise ValueError(f"out_dtype: {dtype}, expected torch.float32 or torch.bfloat16")
+    return _OUT[dtype]
+
+
+def quantize(x: torch.Tensor):
+    """(codes uint8 [..., K/2], scales uint8 [..., K/32]) of fp32, bf16 or fp16 values [..., K], K a multiple of 32."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x: expected a tensor [..., K]")
+    K = x.shape[-1]
+    _require(x, "x", x.shape, tuple(_DTYPES))
+    if K == 0 or K % 32:
+        raise ValueError(f"x: the last dimension is {K}, expected a multiple of 32")
+    _same_device([("x", x)])
+    lead, rows = x.shape[:-1], x.numel() // K
+    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
+    _launch(x.device, lib.tmoe_mxfp4_quantize, "tmoe_mxfp4_quantize", x.data_ptr(), _DTYPES[x.dtype], rows, K,
+            codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def _operand(codes, scales, name: str, dim: Optional[int] = None) -> int:
+    """K of an MXFP4 tensor, after checking its two parts against each other."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() < 1 or (dim is not None and codes.dim() != dim):
+        raise ValueError(f"{name}: expected a tensor of codes" + (f" with {dim} dimensions" if dim else ""))
+    K = 2 * codes.shape[-1]
+    if K == 0 or K % 32:
+        raise ValueError(f"{name}: rows of {K} values, expected a multiple of 32")
+    _require(codes, f"{name} codes", codes.shape, (torch.uint8,))
+    _require(scales, f"{name} scales", (*codes.shape[:-1], K // 32), (torch.uint8,))
+    return K
+
+
+def dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float32) -> torch.Tensor:
+    """The values [..., K] of codes [..., K/2] and scales [..., K/32], rounded once to `dtype`."""
+    K = _operand(codes, scales, "x")
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype: {dtype}, expected one of {[str(d) for d in _DTYPES]}")
+    _same_device([("codes", codes), ("scales", scales)])
+    x = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
+    _launch(codes.device, lib.tmoe_mxfp4_dequantize, "tmoe_mxfp4_dequantize", codes.data_ptr(), scales.data_ptr(),
+            x.numel() // K, K, _DTYPES[dtype], x.data_ptr())
+    return x
+
+
+def linear(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+           out_dtype=torch.float32, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [T, N] = X W^T of MXFP4 X [T, K] and W [N, K] (fp32 sums, rounded once to out_dtype)."""
+    K = _operand(x_codes, x_scales, "x", 2)
+    if _operand(w_codes, w_scales, "w", 2) != K:
+        raise ValueError(f"w: rows of {2 * w_codes.shape[1]} values, x has {K}")
+    T, N, out = x_codes.shape[0], w_codes.shape[0], _out_dtype(out_dtype)
+    if y is None:
+        y = torch.empty((T, N), dtype=out_dtype, device=x_codes.device)
+    else:
+        _require(y, "y", (T, N), (out_dtype,))
+    _same_device([("x codes", x_codes), ("x scales", x_scales), ("w codes", w_codes), ("w scales", w_scales), ("y", y)])
+    _launch(y.device, lib.tmoe_linear_mxfp4, "tmoe_linear_mxfp4", x_codes.data_ptr(), x_scales.data_ptr(), T,
+            w_codes.data_ptr(), w_scales.data_ptr(), K, N, out, y.data_ptr())
+    return y
+
+
+class ExpertWeights:
+    """MXFP4 weights of E experts: w1 [E, 2I, H/2] and s1 [E, 2I, H/32] (gate rows first), w2 [E, H, I/2] and
+    s2 [E, H, I/32], uint8 tensors on one GPU."""
+
+    FIELDS = ("w1", "s1", "w2", "s2")
+
+    def __init__(self, w1: torch.Tensor, s1: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor):
+        self.w1, self.s1, self.w2, self.s2 = w1, s1, w2, s2
+
+    @property
+    def c(self) -> native.Mxfp4Weights:
+        return native.Mxfp4Weights(self.w1.data_ptr(), self.s1.data_ptr(), self.w2.data_ptr(), self.s2.data_ptr())
+
+
+class ExpertPlan:
+    """The routed expert layer with MXFP4 weights and activations (tmoe_forward_mxfp4)."""
+
+    def __init__(self, hidden: int, inter: int, num_experts: int, top_k: int, max_tokens: int, ids_dtype=torch.int64,
+                 out_dtype=torch.float32):
+        if ids_dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"ids_dtype: {ids_dtype}, expected torch.int32 or torch.int64")
+        self.config = native.Mxfp4Config(hidden, inter, num_experts, top_k, max_tokens,
+                                         native.IDS_I64 if ids_dtype == torch.int64 else native.IDS_I32,
+                                         _out_dtype(out_dtype))
+        handle, sb = ctypes.c_void_p(), ctypes.c_size_t()
+        check(lib.tmoe_mxfp4_plan(ctypes.byref(self.config), ctypes.byref(handle), ctypes.byref(sb)), "tmoe_mxfp4_plan")
+        self.handle, self.scratch_bytes = handle, sb.value
+        self.hidden, self.inter, self.num_experts, self.top_k = hidden, inter, num_experts, top_k
+        self.max_tokens, self.ids_dtype, self.out_dtype = max_tokens, ids_dtype, out_dtype
+
+    def close(self):
+        if getattr(self, "handle", None) and self.handle.value:
+            lib.tmoe_mxfp4_plan_destroy(self.handle)
+            self.handle = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def alloc_scratch(self, device="cuda") -> torch.Tensor:
+        return torch.empty(self.scratch_bytes, dtype=torch.uint8, device=device)
+
+    def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, weights: ExpertWeights,
+                scratch: torch.Tensor, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """y [T, H] of x bf16 [T, H] (or its bit patterns), ids [T, k], w fp32 [T, k]."""
+        T = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else -1
+        if y is None and isinstance(x, torch.Tensor):
+            y = torch.empty((max(T, 0), self.hidden), dtype=self.out_dtype, device=x.device)
+        self.check_call(x, ids, w, weights, scratch, y)
+        _launch(x.device, lib.tmoe_forward_mxfp4, "tmoe_forward_mxfp4", self.handle, x.data_ptr(), ids.data_ptr(),
+                w.data_ptr(), T, ctypes.byref(weights.c), y.data_ptr(), scratch.data_ptr(), scratch.numel())
+        return y
+
+    def check_call(self, x, ids, w, weights, scratch, y) -> None:
+        """Raise ValueError unless the tensors match what the forward reads and writes, all contiguous and on
+        one GPU device."""
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x: expected a 2-D tensor [T, H]")
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"x: {T} tokens, the plan holds at most {self.max_tokens}")
+        H, I, E, k = self.hidden, self.inter, self.num_experts, self.top_k
+        _require(x, "x", (T, H), _BITS16)
+        _require(ids, "ids", (T, k), (self.ids_dtype,))
+        _require(w, "w", (T, k), (torch.float32,))
+        _require(y, "y", (T, H), (self.out_dtype,))
+        if not isinstance(weights, ExpertWeights):
+            raise ValueError("weights: expected ExpertWeights")
+        for name, shape in (("w1", (E, 2 * I, H // 2)), ("s1", (E, 2 * I, H // 32)), ("w2", (E, H, I // 2)),
+                            ("s2", (E, H, I // 32))):
+            _require(getattr(weights, name), name, shape, (torch.uint8,))
+        _check_scratch(scratch, self.scratch_bytes)
+        _same_device([("x", x), ("ids", ids), ("w", w), ("y", y), ("scratch", scratch)]
+                     + [(n, getattr(weights, n)) for n in ExpertWeights.FIELDS])

@@ -27,7 +27,9 @@ EXPORTS = ["tmoe_plan", "tmoe_plan_destroy", "tmoe_plan_get_info", "tmoe_plan_ex
            "tmoe_status_str",
            "tmoe_debug_decode", "tmoe_debug_mxfp8", "tmoe_debug_rotate", "tmoe_debug_get_views",
            "tmoe_linear_plan", "tmoe_linear_plan_destroy", "tmoe_linear_w4a16",
-           "tmoe_router_topk", "tmoe_balance_loss_scratch", "tmoe_balance_loss", "tmoe_router_backward"]
+           "tmoe_router_topk", "tmoe_balance_loss_scratch", "tmoe_balance_loss", "tmoe_router_backward",
+           "tmoe_mxfp4_quantize", "tmoe_mxfp4_dequantize", "tmoe_linear_mxfp4", "tmoe_mxfp4_plan",
+           "tmoe_mxfp4_plan_destroy", "tmoe_forward_mxfp4"]
 
 
 class Config(ctypes.Structure):
@@ -74,6 +76,15 @@ class RouterConfig(ctypes.Structure):
                 ("ids_dtype", ctypes.c_int32), ("renormalize", ctypes.c_int32)]
 
 
+class Mxfp4Config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "num_experts", "top_k", "max_tokens", "ids_dtype",
+                                              "y_dtype")]
+
+
+class Mxfp4Weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "s1", "w2", "s2")]
+
+
 class TmoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}")
@@ -117,6 +128,12 @@ def _load():
     lib.tmoe_balance_loss_scratch.argtypes = [RC, I32, ctypes.POINTER(SZ)]
     lib.tmoe_balance_loss.argtypes = [RC, P, I64, P, P, I32, F, P, P, P, P, SZ, P]
     lib.tmoe_router_backward.argtypes = [RC, P, I64, P, P, P, P, P, P, I32, P, P]
+    lib.tmoe_mxfp4_quantize.argtypes = [P, I32, I64, I32, P, P, P]
+    lib.tmoe_mxfp4_dequantize.argtypes = [P, P, I64, I32, I32, P, P]
+    lib.tmoe_linear_mxfp4.argtypes = [P, P, I32, P, P, I32, I32, I32, P, P]
+    lib.tmoe_mxfp4_plan.argtypes = [ctypes.POINTER(Mxfp4Config), ctypes.POINTER(P), ctypes.POINTER(SZ)]
+    lib.tmoe_mxfp4_plan_destroy.argtypes = [P]
+    lib.tmoe_forward_mxfp4.argtypes = [P, P, P, P, I32, ctypes.POINTER(Mxfp4Weights), P, P, SZ, P]
     for name in EXPORTS:
         if name != "tmoe_status_str":
             getattr(lib, name).restype = I32
