@@ -24,8 +24,9 @@ struct BalanceArgs {
   int groups;                // workgroups of the first launch
   int rows_per_group;
   float coefficient;
-  float* psum;               // [groups][E] sums of probabilities
-  int32_t* csum;             // [groups][E] routes per expert
+  int pitch;                 // E rounded up to a multiple of 4
+  float* psum;               // [groups][pitch] sums of probabilities
+  int32_t* csum;             // [groups][pitch] routes per expert
   int32_t* nsum;             // [groups] rows that count
   float* loss;               // [1]
   int32_t* counts;           // [E]
@@ -45,7 +46,7 @@ struct RouterGradArgs {
   void* dlogits;             // [T][E], the logits' type
 };
 
-constexpr int kBalanceMaxGroups = 512;
+constexpr int kBalanceMaxGroups = 256;   // one workgroup of 16 wavefronts a CU (at most 1024: the second launch's threads)
 
 // dtype: TMOE_F32, TMOE_BF16 or TMOE_F16
 void launch_router_topk(const RouterTopkArgs& a, int dtype, hipStream_t s);

@@ -41,19 +41,20 @@ tmoe_status check_rows(const tmoe_router_config* c, const void* logits, int64_t 
 }
 
 struct BalanceShape {
-  int groups, rows;
+  int groups, rows, pitch;
   size_t psum, csum, nsum, total;                // arena offsets
 };
 
 BalanceShape balance_shape(int T, int E) {
   BalanceShape b;
-  // at least four rows (one a wavefront) per workgroup, at most kBalanceMaxGroups workgroups
-  b.rows = std::max(4, (T + kBalanceMaxGroups - 1) / kBalanceMaxGroups);
+  // at least 16 rows (one a wavefront) per workgroup, at most kBalanceMaxGroups workgroups
+  b.pitch = (E + 3) / 4 * 4;
+  b.rows = std::max(16, (T + kBalanceMaxGroups - 1) / kBalanceMaxGroups);
   b.groups = (T + b.rows - 1) / b.rows;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   b.psum = 0;
-  b.csum = up(4ull * b.groups * E);
-  b.nsum = b.csum + up(4ull * b.groups * E);
+  b.csum = up(4ull * b.groups * b.pitch);
+  b.nsum = b.csum + up(4ull * b.groups * b.pitch);
   b.total = b.nsum + up(4ull * b.groups);
   return b;
 }
@@ -120,6 +121,7 @@ tmoe_status tmoe_balance_loss(const tmoe_router_config* c, const void* logits, i
   a.ids64 = c->ids_dtype == TMOE_IDS_I64;
   a.groups = b.groups;
   a.rows_per_group = b.rows;
+  a.pitch = b.pitch;
   a.coefficient = coefficient;
   char* base = static_cast<char*>(scratch);
   a.psum = reinterpret_cast<float*>(base + b.psum);
