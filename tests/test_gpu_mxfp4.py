@@ -113,11 +113,30 @@ def test_linear(T, K, N, dtype):
     assert np.all(err <= bound + HALF[dtype] * (np.abs(ref) + bound)), float((err / (bound + 1e-30)).max())
 
 
-@pytest.mark.parametrize("T", [1, 16, 40, 300])
+@pytest.mark.parametrize("T,K,N", [(2000, 160, 2100), (2049, 544, 1800), (1793, 640, 2305), (2048, 512, 2048),
+                                   (1900, 1152, 2100), (4100, 96, 1030), (2048, 2080, 2048)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_many_rows_and_columns(T, K, N, dtype):
+    test_linear(T, K, N, dtype)
+
+
+def test_linear_unaligned_scales():
+    """Scales of a K that is a multiple of 128, but not at a 4-byte address."""
+    rng = np.random.default_rng(3)
+    T, K, N = 2048, 640, 2048
+    xq, xs, x = M.random_operand(rng, T, K)
+    wq, ws, w = M.random_operand(rng, N, K)
+    odd = torch.empty(T * K // 32 + 1, dtype=torch.uint8, device="cuda")
+    odd[1:] = _gpu(xs).flatten()
+    y = _mx().linear(_gpu(xq), odd[1:].view(T, K // 32), _gpu(wq), _gpu(ws)).cpu().numpy()
+    assert np.all(np.abs(y - x @ w.T) <= M.product_slack(K) * (np.abs(x) @ np.abs(w).T))
+
+
+@pytest.mark.parametrize("T", [1, 16, 40, 300, 2300])
 def test_linear_operand_layout_is_exact(T):
     """Small whole numbers times powers of two: every sum is exact, so a value in a wrong place shows."""
     rng = np.random.default_rng(T)
-    K, N = 288, 96
+    K, N = 288, 96 if T < 1000 else 2000
     code = rng.integers(0, 16, size=(T, K)).astype(np.uint8)
     xs = rng.integers(124, 131, size=(T, K // 32)).astype(np.uint8)
     wcode = rng.integers(0, 16, size=(N, K)).astype(np.uint8)

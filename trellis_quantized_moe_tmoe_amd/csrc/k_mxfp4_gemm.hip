@@ -13,14 +13,9 @@ namespace tmoe {
 namespace {
 
 typedef int i4v __attribute__((ext_vector_type(4)));
+typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 
 enum { kDenseF32 = 0, kDenseBf16 = 1, kFc1 = 2, kFc2 = 3 };
-
-__device__ __forceinline__ uint16_t bf16_rne(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return static_cast<uint16_t>((u >> 16) | 0x40u);
-  return static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
-}
 
 __device__ __forceinline__ f4 mma(i4v w, int ws, i4v x, int xs, f4 c) {
   const i8v a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -44,6 +39,31 @@ __device__ __forceinline__ Frag load_block(const uint8_t* q, const uint8_t* s, i
     f.s = 127;
   }
   return f;
+}
+
+// Four neighbouring columns col.. of a row of N, at element `at` of y; columns past N are dropped. QUADS: N
+// is a multiple of four, so a quad is whole and aligned.
+template <bool BF16, bool QUADS>
+__device__ __forceinline__ void store4(void* y, long long at, int col, int N, f4 v) {
+  if constexpr (BF16) {
+    uint16_t* o = static_cast<uint16_t*>(y) + at;
+    if constexpr (QUADS) {                                 // both round to nearest even
+      if (col < N) *reinterpret_cast<bf4*>(o) = __builtin_convertvector(v, bf4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < N) o[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
+    }
+  } else {
+    float* o = static_cast<float*>(y) + at;
+    if constexpr (QUADS) {
+      if (col < N) *reinterpret_cast<f4*>(o) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < N) o[i] = v[i];
+    }
+  }
 }
 
 // silu(g) * u, then the MXFP4 block of 32 neighbouring columns: a lane holds four of them in each of two
@@ -171,32 +191,322 @@ __global__ __launch_bounds__(256) void k_mxfp4_direct(Mxfp4GemmArgs a) {
       for (int n = 0; n < NT; ++n) {
         const int col = 16 * NT * group + 16 * n + 4 * q;
         if (!live) continue;
-        const long long at = row * a.N + col;
-        if constexpr (MODE == kDenseBf16) {
-          uint16_t* y = static_cast<uint16_t*>(a.y) + at;
-          uint16_t b[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) b[i] = bf16_rne(acc[m][n][i]);
-          if (a.N % 4 == 0 && col < a.N) {
-            *reinterpret_cast<ushort4*>(y) = make_ushort4(b[0], b[1], b[2], b[3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (col + i < a.N) y[i] = b[i];
-          }
-        } else {
-          float* y = static_cast<float*>(a.y) + at;
-          if (a.N % 4 == 0 && col < a.N) {
-            *reinterpret_cast<f4*>(y) = acc[m][n];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (col + i < a.N) y[i] = acc[m][n][i];
-          }
-        }
+        if (a.N % 4 == 0) store4<MODE == kDenseBf16, true>(a.y, row * a.N + col, col, a.N, acc[m][n]);
+        else store4<MODE == kDenseBf16, false>(a.y, row * a.N + col, col, a.N, acc[m][n]);
       }
     }
   }
+}
+
+// ---------------------------------------------------------------- tiles through LDS
+// A workgroup of four wavefronts computes 32 MT WT rows by 32 NT WC columns with
+// v_mfma_scale_f32_32x32x64_f8f6f4: a lane holds row l % 32 of a fragment and one 16-byte block of it;
+// in sub-step s of a 128-deep step the lanes of half h = l / 32 take block 2 h + s (the sum does not
+// care which half takes which block), so a lane's two scale bytes of a step are neighbours.
+//
+// Codes go from global memory straight to a ring of kDepth LDS slots, one 128-deep step each, 64 bytes a
+// row. The 16-byte chunk c of row r lies at place c ^ swizzle(r), so that the 16-byte reads of any 8 or
+// 16 neighbouring rows touch every bank once; the copy writes LDS in lane order, so the swizzle is in
+// the lane's global address. Scales come as 16 bytes (four steps) a row through registers, two buffers
+// of them. Blocks past K repeat the codes of the last block and get the scale 2^-127 in both operands: their
+// products, at most 36 * 2^-254 each, vanish in an fp32 sum.
+//
+// A step has two sub-steps of 64; each multiplies fragments that were read from LDS during the one
+// before. One barrier a step, between its sub-steps: by then every wavefront has read the step's slot, so
+// the copy of step ks + kDepth goes there.
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+constexpr int kDepth = 4;
+
+__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
+
+template <int SUB>
+__device__ __forceinline__ f16v mma32(i4v w, int ws, i4v x, int xs, f16v c) {
+  const i8v a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+  const i8v b = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, SUB, ws, SUB, xs);
+}
+
+template <int MODE, int WT, int WC, int MT, int NT>
+struct Tile {
+  static constexpr int TR = 32 * MT * WT, TC = 32 * NT * WC;      // rows (tokens) and columns
+  static constexpr int kSlot = (TR + TC) * 64;                    // bytes of one ring slot
+  static constexpr int kScales = (TR + TC) * 16;                  // bytes of one scale buffer
+  static constexpr int kLds = kDepth * kSlot + 2 * kScales;
+  static constexpr int LPS = (TR + TC) / 64;                      // copies a wavefront issues a step
+  static constexpr int SPT = (TR + TC + 255) / 256;               // scale rows a thread stages
+};
+
+// silu(g) * u of 32 neighbouring columns of one token and their MXFP4 block: a lane holds the columns
+// 8 i + 4 h + [0, 4), the lane 32 away the others.
+__device__ __forceinline__ void store_swiglu32(const f16v& g, const f16v& u, uint8_t* bq, uint8_t* bs, int h, bool store) {
+  float v[16];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float x = g[i];
+    v[i] = x / (1.0f + expf(-x)) * u[i];
+    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+    m = b > m ? b : m;
+  }
+  const uint32_t o = __shfl_xor(m, 32, 64);
+  m = o > m ? o : m;
+  const uint32_t byte = mxfp4_scale_byte(m);
+  const float inv = mxfp4_inverse_scale(byte);
+  uint32_t c[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = v[8 * p + i] * inv;
+    c[p] = byte == 255u ? 0u : mxfp4_codes8(w);
+  }
+  // half 0 stores columns 0..15, half 1 columns 16..31: each gives the other what it holds of them
+  const uint32_t other = __shfl_xor(h ? c[0] : c[1], 32, 64);
+  const uint32_t own = h ? c[1] : c[0];
+  const uint32_t even = h ? other : own, odd = h ? own : other;   // columns 8 i + [0, 4) and 8 i + [4, 8)
+  if (store) {
+    reinterpret_cast<uint2*>(bq)[h] = make_uint2((even & 0xffffu) | (odd << 16), (even >> 16) | (odd & 0xffff0000u));
+    if (h == 0) *bs = static_cast<uint8_t>(byte);
+  }
+}
+
+// ALIGNED: K is a multiple of 128 and at least 512 and the scales are 4-byte aligned. Their rows are then copied
+// straight to LDS like the codes; else they pass through registers, whose wait (the compiler's, for every
+// copy in flight) costs a stall in each group of four steps.
+template <int MODE, int WT, int WC, int MT, int NT, bool ALIGNED>
+__device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expert, int row0, int nrows, int cg,
+                                          uint8_t* lds) {
+  using S = Tile<MODE, WT, WC, MT, NT>;
+  static_assert(WT * WC == 4 && (MODE != kFc1 || NT == 2), "four wavefronts; first product: gate and up fragment");
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r32 = lane & 31, h = lane >> 5;
+  const int wt = wv / WC, wc = wv % WC;
+  const int nblk = a.K / 32, steps = (nblk + 3) / 4;
+  const uint8_t* wq = a.wq + expert * a.N * (a.K / 2);
+  const uint8_t* ws = a.ws + expert * a.N * nblk;
+  const int inter = a.N / 2;
+
+  // global row of a tile row i: tokens first, then weight rows; rows past the end repeat the last one
+  auto source = [&](int i, bool scales) -> const uint8_t* {
+    if (i < S::TR) {
+      long long row = row0 + min(i, nrows - 1);
+      if constexpr (MODE == kFc1) row = a.sorted[row] / a.top_k;
+      return scales ? a.xs + row * nblk : a.xq + row * (a.K / 2);
+    }
+    const int j = i - S::TR;
+    long long col;
+    if constexpr (MODE == kFc1) col = ((j >> 5) & 1) * inter + min(cg * (S::TC / 2) + (j >> 6) * 32 + (j & 31), inter - 1);
+    else col = min(cg * S::TC + j, a.N - 1);
+    return scales ? ws + col * nblk : wq + col * (a.K / 2);
+  };
+  const uint8_t* src[S::LPS];
+#pragma unroll
+  for (int i = 0; i < S::LPS; ++i) src[i] = source(16 * (wv + 4 * i) + (lane >> 2), false);
+  const uint8_t* ssrc[S::SPT];
+#pragma unroll
+  for (int i = 0; i < S::SPT; ++i) {
+    if constexpr (ALIGNED) ssrc[i] = source(64 * min(wv + 4 * i, (S::TR + S::TC) / 64 - 1) + lane, true);
+    else ssrc[i] = nblk >= 16 ? source(min(tid + 256 * i, S::TR + S::TC - 1), true) : a.wq;
+  }
+  const int chunk = (lane & 3) ^ swizzle(lane >> 2);
+
+  auto issue = [&](int ks, int i) {              // one of a wavefront's LPS copies (16 rows) of step ks
+    const int blk = min(4 * ks + chunk, nblk - 1);
+    __builtin_amdgcn_global_load_lds(
+        (const void __attribute__((address_space(1)))*)(src[i] + 16 * blk),
+        (void __attribute__((address_space(3)))*)(lds + (ks % kDepth) * S::kSlot + (wv + 4 * i) * 1024), 16, 0, 0);
+  };
+  // Scales of steps 4 g .. 4 g + 3: bytes 16 g .. of each row. The last group's load starts where it ends with
+  // the row and is shifted when it is stored; rows shorter than 16 bytes have one
+  // group, read byte by byte before the loop (the loop's fetches then read 16 bytes of codes for nothing).
+  auto copy_scales = [&](int g) {                // ALIGNED: 64 rows of 16 bytes a copy, repeats at the end
+    const int from = min(16 * g, nblk - 16);
+#pragma unroll
+    for (int i = 0; i < S::SPT; ++i)
+      __builtin_amdgcn_global_load_lds(
+          (const void __attribute__((address_space(1)))*)(ssrc[i] + from),
+          (void __attribute__((address_space(3)))*)(lds + kDepth * S::kSlot + (g & 1) * S::kScales +
+                                                    min(wv + 4 * i, (S::TR + S::TC) / 64 - 1) * 1024),
+          16, 0, 0);
+  };
+  uint4 sreg[S::SPT];
+  auto load_scales = [&](int g) {
+    const int from = nblk >= 16 ? min(16 * g, nblk - 16) : 0;
+#pragma unroll
+    for (int i = 0; i < S::SPT; ++i) __builtin_memcpy(&sreg[i], ssrc[i] + from, 16);
+  };
+  auto store_scales = [&](int g) {               // no branches: the loop body stays one block
+    uint8_t* buf = lds + kDepth * S::kSlot + (g & 1) * S::kScales;
+    const int by = max(16 * g - (nblk - 16), 0);   // bytes to shift out: 8 and 4 by masks, the rest by alignbyte
+    uint32_t keep[2] = {by & 8 ? 0u : ~0u, by & 4 ? 0u : ~0u};
+    asm("" : "+v"(keep[0]), "+v"(keep[1]));      // opaque: selects on a known condition become branches
+#pragma unroll
+    for (int i = 0; i < S::SPT; ++i) {
+      uint32_t w[4] = {sreg[i].x, sreg[i].y, sreg[i].z, sreg[i].w};
+#pragma unroll
+      for (int d = 2; d; d >>= 1)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t m = keep[2 - d];
+          w[q] = (w[q] & m) | (q + d < 4 ? w[q + d] & ~m : 0u);
+        }
+      const uint32_t b = by & 3;
+      reinterpret_cast<uint4*>(buf)[min(tid + 256 * i, S::TR + S::TC - 1)] =
+          make_uint4(__builtin_amdgcn_alignbyte(w[1], w[0], b), __builtin_amdgcn_alignbyte(w[2], w[1], b),
+                     __builtin_amdgcn_alignbyte(w[3], w[2], b), __builtin_amdgcn_alignbyte(0u, w[3], b));
+    }
+  };
+  auto first_scales = [&]() {
+    if (nblk >= 16) {
+      load_scales(0);
+      store_scales(0);
+      return;
+    }
+    uint8_t* buf = lds + kDepth * S::kSlot;
+    for (int i = tid; i < S::TR + S::TC; i += 256) {
+      const uint8_t* p = source(i, true);
+      for (int b = 0; b < 16; ++b) buf[16 * i + b] = b < nblk ? p[b] : 0;
+    }
+  };
+
+  struct Frags {                                 // one sub-step
+    i4v x[MT], w[NT];
+  };
+  const int place = swizzle(r32);
+  const int lane0 = 64 * r32 + 16 * ((2 * h) ^ place), lane1 = 64 * r32 + 16 * ((2 * h + 1) ^ place);
+  // Piece p of MT reads fragment row p and its share of the columns of sub-step s (and, with SCALES, their
+  // scales) of step ks.
+  int xs[MT], ws4[NT], nx[MT], nw[NT];
+  auto read_piece = [&](int ks, int s, int p, Frags& f, bool scales) {
+    const uint8_t* slot = lds + (ks % kDepth) * S::kSlot + (s ? lane1 : lane0);
+    // ALIGNED: the last group's bytes start where they end with the row
+    const int at = ALIGNED ? min(4 * ks - min(16 * (ks >> 2), nblk - 16), 12) : 4 * (ks & 3);
+    const uint8_t* sc = lds + kDepth * S::kSlot + ((ks >> 2) & 1) * S::kScales + 16 * r32 + at + 2 * h;
+    f.x[p] = *reinterpret_cast<const i4v*>(slot + 2048 * (wt * MT + p));
+    if (scales) nx[p] = *reinterpret_cast<const uint16_t*>(sc + 512 * (wt * MT + p));
+#pragma unroll
+    for (int n = p * NT / MT; n < (p + 1) * NT / MT; ++n) {
+      f.w[n] = *reinterpret_cast<const i4v*>(slot + 64 * S::TR + 2048 * (wc * NT + n));
+      if (scales) nw[n] = *reinterpret_cast<const uint16_t*>(sc + 16 * S::TR + 512 * (wc * NT + n));
+    }
+  };
+
+  f16v acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n] = f16v{};
+
+  if constexpr (ALIGNED) copy_scales(0);
+  else first_scales();
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d)
+#pragma unroll
+    for (int i = 0; i < S::LPS; ++i) issue(d, i);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::LPS * (kDepth - 1)) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frags f0, f1;
+#pragma unroll
+  for (int p = 0; p < MT; ++p) read_piece(0, 0, p, f0, true);
+
+  // Copies past the last step repeat its last block and reads of step `steps` see one of those: neither is
+  // used, and every step looks the same. PHASE: ks % 4; the next group's scales are fetched during step 0
+  // and stored during step 2. The order within a step is pinned: each fragment row's matrix instructions
+  // stand behind the reads and copies that run beneath them (left free, the compiler gathers all matrix
+  // instructions of four steps behind all reads).
+  auto step = [&](int ks, auto phase) {
+    constexpr int PHASE = decltype(phase)::value;
+    const int mask = !ALIGNED || 4 * ks < nblk ? 0xffff : 0;   // ALIGNED: steps past K read any scale
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xs[m] = nx[m] & mask;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) ws4[n] = nw[n] & mask;
+    if constexpr (PHASE == 0 && ALIGNED) copy_scales((ks >> 2) + 1);
+    if constexpr (PHASE == 0 && !ALIGNED) load_scales((ks >> 2) + 1);
+    if constexpr (PHASE == 2 && !ALIGNED) store_scales((ks >> 2) + 1);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      read_piece(ks, 1, m, f1, false);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n] = mma32<0>(f0.w[n], ws4[n], f0.x[m], xs[m], acc[m][n]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // Step ks + 1 has landed: the copies of steps ks + 2 and ks + 3 may still be in flight, and the scales'
+    // that were issued after those of ks + 1 (steps 0 and 1 of a group; other loads among them would only
+    // make the wait stricter), and this wavefront's LDS accesses are done. Behind the barrier that holds for
+    // all four wavefronts: the slot of step ks is free. The next group's scales are read from the middle of
+    // step 3 on: step 2's wait covers them.
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::LPS * (kDepth - 2) + (ALIGNED && PHASE < 2 ? S::SPT : 0))
+                 : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      read_piece(ks + 1, 0, m, f0, true);
+#pragma unroll
+      for (int i = m * S::LPS / MT; i < (m + 1) * S::LPS / MT; ++i) issue(ks + kDepth, i);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n] = mma32<1>(f1.w[n], ws4[n], f1.x[m], xs[m], acc[m][n]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  for (int ks = 0; ks < steps; ks += 4) {        // whole groups of four: steps past K add nothing
+    step(ks, std::integral_constant<int, 0>{});
+    step(ks + 1, std::integral_constant<int, 1>{});
+    step(ks + 2, std::integral_constant<int, 2>{});
+    step(ks + 3, std::integral_constant<int, 3>{});
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the copies past the end land before LDS is given up
+
+  if constexpr (MODE == kFc1) {
+    const int col = cg * (S::TC / 2) + 32 * wc;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int i = 32 * (wt * MT + m) + r32;
+      const long long row = row0 + i;
+      store_swiglu32(acc[m][0], acc[m][1], a.bq + row * (inter / 2) + col / 2, a.bs + row * (inter / 32) + col / 32, h,
+                     i < nrows && col < inter);
+    }
+  } else {
+    auto store = [&](auto whole) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int i = 32 * (wt * MT + m) + r32;
+        const long long row = static_cast<long long>(row0 + i) * a.N;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int col = cg * S::TC + 32 * (wc * NT + n) + 8 * q + 4 * h;
+            const f4 v = {acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
+            if (i < nrows) store4<MODE == kDenseBf16, decltype(whole)::value>(a.y, row + col, col, a.N, v);
+          }
+      }
+    };
+    if (a.N % 4 == 0) store(std::true_type{});
+    else store(std::false_type{});
+  }
+}
+
+// Dense: row tiles by column tiles in groups of eight row tiles, a contiguous run of them to each of the
+// eight XCDs (workgroups are dealt to the XCDs in turn), so that an XCD's L2 holds what its tiles share.
+template <int MODE, int WT, int WC, int MT, int NT, bool ALIGNED>
+__global__ __launch_bounds__(256, 1) void k_mxfp4_tile_dense(Mxfp4GemmArgs a, int row_tiles, int col_tiles) {
+  using S = Tile<MODE, WT, WC, MT, NT>;
+  __shared__ __align__(16) uint8_t lds[S::kLds];
+  const int total = row_tiles * col_tiles, per = gridDim.x / 8;
+  const int t = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  if (t >= total) return;
+  constexpr int G = 8;
+  const int g = t / (G * col_tiles), in = t % (G * col_tiles);
+  const int rows_g = min(G, row_tiles - g * G);
+  const int rt = g * G + in % rows_g, ct = in / rows_g;
+  const int row0 = rt * S::TR;
+  tile_body<MODE, WT, WC, MT, NT, ALIGNED>(a, 0, row0, min(S::TR, a.rows - row0), ct, lds);
 }
 
 // y_t = sum over j ascending of w[t][j] * v[slot of (t, j)], four columns a thread.
@@ -214,7 +524,7 @@ __global__ __launch_bounds__(256) void k_mxfp4_combine(Mxfp4CombineArgs a) {
     s += a.w[t * a.top_k + j] * reinterpret_cast<const f4*>(a.v + static_cast<long long>(slot) * a.H)[c];
   }
   if constexpr (BF16)
-    static_cast<ushort4*>(a.y)[i] = make_ushort4(bf16_rne(s[0]), bf16_rne(s[1]), bf16_rne(s[2]), bf16_rne(s[3]));
+    static_cast<bf4*>(a.y)[i] = __builtin_convertvector(s, bf4);
   else
     static_cast<f4*>(a.y)[i] = s;
 }
@@ -230,7 +540,24 @@ void launch_direct(const Mxfp4GemmArgs& a, bool small, int tiles, hipStream_t s)
   else hipLaunchKernelGGL((k_mxfp4_direct<MODE, 4, 4, 1>), dim3((cols + 3) / 4 * tiles), dim3(256), 0, s, a);
 }
 
+bool scales_aligned(const Mxfp4GemmArgs& a) {
+  return a.K % 128 == 0 && a.K >= 512 &&
+         ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
+}
+
 void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s) {
+  const int rt = (a.rows + 255) / 256, ct = (a.N + 255) / 256;
+  if (rt * ct >= 64) {
+    const dim3 g((rt * ct + 7) / 8 * 8);
+    auto go = [&](auto bf, auto al) {
+      constexpr int MODE = decltype(bf)::value ? kDenseBf16 : kDenseF32;
+      hipLaunchKernelGGL((k_mxfp4_tile_dense<MODE, 2, 2, 4, 4, decltype(al)::value>), g, dim3(256), 0, s, a, rt, ct);
+    };
+    const bool al = scales_aligned(a);
+    if (y_dtype == TMOE_BF16) al ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+    else al ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+    return;
+  }
   const bool small = a.rows <= 16;
   const int tiles = small ? 1 : (a.rows + 63) / 64;
   if (y_dtype == TMOE_BF16) launch_direct<kDenseBf16>(a, small, tiles, s);
