@@ -375,20 +375,21 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
   };
   const int place = swizzle(r32);
   const int lane0 = 64 * r32 + 16 * ((2 * h) ^ place), lane1 = 64 * r32 + 16 * ((2 * h + 1) ^ place);
-  // Piece p of MT reads fragment row p and its share of the columns of sub-step s (and, with SCALES, their
-  // scales) of step ks.
+  // Piece p of MT + NT reads one fragment of sub-step s of step ks (and, with SCALES, its scales): the columns
+  // first, which every matrix instruction of the first row needs.
   int xs[MT], ws4[NT], nx[MT], nw[NT];
   auto read_piece = [&](int ks, int s, int p, Frags& f, bool scales) {
     const uint8_t* slot = lds + (ks % kDepth) * S::kSlot + (s ? lane1 : lane0);
     // ALIGNED: the last group's bytes start where they end with the row
     const int at = ALIGNED ? min(4 * ks - min(16 * (ks >> 2), nblk - 16), 12) : 4 * (ks & 3);
     const uint8_t* sc = lds + kDepth * S::kSlot + ((ks >> 2) & 1) * S::kScales + 16 * r32 + at + 2 * h;
-    f.x[p] = *reinterpret_cast<const i4v*>(slot + 2048 * (wt * MT + p));
-    if (scales) nx[p] = *reinterpret_cast<const uint16_t*>(sc + 512 * (wt * MT + p));
-#pragma unroll
-    for (int n = p * NT / MT; n < (p + 1) * NT / MT; ++n) {
-      f.w[n] = *reinterpret_cast<const i4v*>(slot + 64 * S::TR + 2048 * (wc * NT + n));
-      if (scales) nw[n] = *reinterpret_cast<const uint16_t*>(sc + 16 * S::TR + 512 * (wc * NT + n));
+    if (p < NT) {
+      f.w[p] = *reinterpret_cast<const i4v*>(slot + 64 * S::TR + 2048 * (wc * NT + p));
+      if (scales) nw[p] = *reinterpret_cast<const uint16_t*>(sc + 16 * S::TR + 512 * (wc * NT + p));
+    } else {
+      const int m = p - NT;
+      f.x[m] = *reinterpret_cast<const i4v*>(slot + 2048 * (wt * MT + m));
+      if (scales) nx[m] = *reinterpret_cast<const uint16_t*>(sc + 512 * (wt * MT + m));
     }
   };
 
@@ -409,13 +410,15 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
   asm volatile("" ::: "memory");
   Frags f0, f1;
 #pragma unroll
-  for (int p = 0; p < MT; ++p) read_piece(0, 0, p, f0, true);
+  for (int p = 0; p < MT + NT; ++p) read_piece(0, 0, p, f0, true);
 
   // Copies past the last step repeat its last block and reads of step `steps` see one of those: neither is
   // used, and every step looks the same. PHASE: ks % 4; the next group's scales are fetched during step 0
-  // and stored during step 2. The order within a step is pinned: each fragment row's matrix instructions
-  // stand behind the reads and copies that run beneath them (left free, the compiler gathers all matrix
-  // instructions of four steps behind all reads).
+  // and stored during step 2. The order within a step is pinned, one or two reads or a copy in front of each
+  // matrix instruction: a wavefront has its SIMD to itself and issues in order, so what does not fit under
+  // the 32 cycles of the instruction before is lost (four of them behind a bunch of reads and copies: 52.9 us
+  // at T = 4096, K = N = 4096; left free, the compiler gathers the matrix instructions of four steps).
+  constexpr int MM = MT * NT, RD = MT + NT;
   auto step = [&](int ks, auto phase) {
     constexpr int PHASE = decltype(phase)::value;
     const int mask = !ALIGNED || 4 * ks < nblk ? 0xffff : 0;   // ALIGNED: steps past K read any scale
@@ -427,11 +430,12 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     if constexpr (PHASE == 0 && !ALIGNED) load_scales((ks >> 2) + 1);
     if constexpr (PHASE == 2 && !ALIGNED) store_scales((ks >> 2) + 1);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      read_piece(ks, 1, m, f1, false);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int j = 0; j < MM; ++j) {
+      constexpr int per = (RD + MM - 1) / MM;    // reads in front of one instruction
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n] = mma32<0>(f0.w[n], ws4[n], f0.x[m], xs[m], acc[m][n]);
+      for (int p = j * per; p < (j + 1) * per && p < RD; ++p) read_piece(ks, 1, p, f1, false);
+      __builtin_amdgcn_sched_barrier(0);
+      acc[j / NT][j % NT] = mma32<0>(f0.w[j % NT], ws4[j % NT], f0.x[j / NT], xs[j / NT], acc[j / NT][j % NT]);
       __builtin_amdgcn_sched_barrier(0);
     }
     // Step ks + 1 has landed: the copies of steps ks + 2 and ks + 3 may still be in flight, and the scales'
@@ -444,13 +448,14 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      read_piece(ks + 1, 0, m, f0, true);
+    for (int j = 0; j < MM; ++j) {
+      constexpr int per = (RD + MM - 1) / MM;
 #pragma unroll
-      for (int i = m * S::LPS / MT; i < (m + 1) * S::LPS / MT; ++i) issue(ks + kDepth, i);
+      for (int p = j * per; p < (j + 1) * per && p < RD; ++p) read_piece(ks + 1, 0, p, f0, true);
+#pragma unroll
+      for (int i = j * S::LPS / MM; i < (j + 1) * S::LPS / MM; ++i) issue(ks + kDepth, i);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n] = mma32<1>(f1.w[n], ws4[n], f1.x[m], xs[m], acc[m][n]);
+      acc[j / NT][j % NT] = mma32<1>(f1.w[j % NT], ws4[j % NT], f1.x[j / NT], xs[j / NT], acc[j / NT][j % NT]);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -472,23 +477,54 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
                      i < nrows && col < inter);
     }
   } else {
-    auto store = [&](auto whole) {
+    // Rows of y are written whole: 32 rows at a time pass through the wavefront's own part of the ring (rows
+    // padded by 16 bytes), so that a store covers 256 or 512 neighbouring bytes of a row (8- or 16-byte
+    // pieces straight from the registers: 22 us of the 52.9 at T = 4096, K = N = 4096).
+    constexpr bool BF = MODE == kDenseBf16;
+    constexpr int ES = BF ? 2 : 4, EPL = 16 / ES, PITCH = 32 * NT * ES + 16;
+    static_assert(4 * 32 * PITCH <= S::kLds, "four wavefronts' rows fit the ring");
+    const int col0 = cg * S::TC + 32 * NT * wc;
+    if (a.N % EPL == 0) {
+      __syncthreads();                           // every wavefront has read its last fragments
+      uint8_t* mine = lds + wv * 32 * PITCH;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int i = 32 * (wt * MT + m) + r32;
-        const long long row = static_cast<long long>(row0 + i) * a.N;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int col = cg * S::TC + 32 * (wc * NT + n) + 8 * q + 4 * h;
             const f4 v = {acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
-            if (i < nrows) store4<MODE == kDenseBf16, decltype(whole)::value>(a.y, row + col, col, a.N, v);
+            uint8_t* to = mine + r32 * PITCH + (32 * n + 8 * q + 4 * h) * ES;
+            if constexpr (BF) *reinterpret_cast<bf4*>(to) = __builtin_convertvector(v, bf4);
+            else *reinterpret_cast<f4*>(to) = v;
           }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        constexpr int LPR = 32 * NT / EPL, RPI = 64 / LPR;     // lanes a row, rows a store
+        const int c = col0 + (lane % LPR) * EPL;
+#pragma unroll
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int r = RPI * i + lane / LPR, row = 32 * (wt * MT + m) + r;
+          const i4v v = *reinterpret_cast<const i4v*>(mine + r * PITCH + (lane % LPR) * 16);
+          if (row < nrows && c < a.N)
+            *reinterpret_cast<i4v*>(static_cast<uint8_t*>(a.y) + (static_cast<long long>(row0 + row) * a.N + c) * ES) = v;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
-    };
-    if (a.N % 4 == 0) store(std::true_type{});
-    else store(std::false_type{});
+      return;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int i = 32 * (wt * MT + m) + r32;
+      const long long row = static_cast<long long>(row0 + i) * a.N;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = col0 + 32 * n + 8 * q + 4 * h;
+          const f4 v = {acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
+          if (i < nrows) store4<BF, false>(a.y, row + col, col, a.N, v);
+        }
+    }
   }
 }
 
