@@ -204,21 +204,20 @@ __global__ __launch_bounds__(256) void k_mxfp4_direct(Mxfp4GemmArgs a) {
 // in sub-step s of a 128-deep step the lanes of half h = l / 32 take block 2 h + s (the sum does not
 // care which half takes which block), so a lane's two scale bytes of a step are neighbours.
 //
-// Codes go from global memory straight to a ring of kDepth LDS slots, one 128-deep step each, 64 bytes a
-// row. The 16-byte chunk c of row r lies at place c ^ swizzle(r), so that the 16-byte reads of any 8 or
-// 16 neighbouring rows touch every bank once; the copy writes LDS in lane order, so the swizzle is in
-// the lane's global address. Scales come as 16 bytes (four steps) a row through registers, two buffers
-// of them. Blocks past K repeat the codes of the last block and get the scale 2^-127 in both operands: their
-// products, at most 36 * 2^-254 each, vanish in an fp32 sum.
+// Codes go from global memory straight to LDS, 256 deep (a pair of steps) at a time into one of two slots: 128
+// bytes a row, so that L2 is asked for whole lines (64-byte pieces, one step at a time into four slots,
+// ran its channels at 60% of their requests: 45.9 us at T = 4096, K = N = 4096). The 16-byte chunk c of row r
+// lies at place c ^ swizzle(r), so that the 16-byte reads of any 8 or 16 neighbouring rows touch every bank
+// once; the copy writes LDS in lane order, so the swizzle is in the lane's global address. Scales come as 16
+// bytes (four steps) a row, two buffers of them. Blocks past K repeat the codes of the last block and get
+// the scale 2^-127 in both operands: their products, at most 36 * 2^-254 each, vanish in an fp32 sum.
 //
 // A step has two sub-steps of 64; each multiplies fragments that were read from LDS during the one
-// before. One barrier a step, between its sub-steps: by then every wavefront has read the step's slot, so
-// the copy of step ks + kDepth goes there.
+// before. One barrier a pair, in the middle of its second step: by then every wavefront has read all of the
+// pair's slot, so the copies of the pair after the next go there.
 typedef float f16v __attribute__((ext_vector_type(16)));
 
-constexpr int kDepth = 4;
-
-__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 7) ^ ((r & 1) << 2); }
 
 template <int SUB>
 __device__ __forceinline__ f16v mma32(i4v w, int ws, i4v x, int xs, f16v c) {
@@ -230,10 +229,10 @@ __device__ __forceinline__ f16v mma32(i4v w, int ws, i4v x, int xs, f16v c) {
 template <int MODE, int WT, int WC, int MT, int NT>
 struct Tile {
   static constexpr int TR = 32 * MT * WT, TC = 32 * NT * WC;      // rows (tokens) and columns
-  static constexpr int kSlot = (TR + TC) * 64;                    // bytes of one ring slot
+  static constexpr int kSlot = (TR + TC) * 128;                   // bytes of one slot
   static constexpr int kScales = (TR + TC) * 16;                  // bytes of one scale buffer
-  static constexpr int kLds = kDepth * kSlot + 2 * kScales;
-  static constexpr int LPS = (TR + TC) / 64;                      // copies a wavefront issues a step
+  static constexpr int kLds = 2 * kSlot + 2 * kScales;
+  static constexpr int LPP = (TR + TC) / 32;                      // copies a wavefront issues a pair
   static constexpr int SPT = (TR + TC + 255) / 256;               // scale rows a thread stages
 };
 
@@ -272,8 +271,8 @@ __device__ __forceinline__ void store_swiglu32(const f16v& g, const f16v& u, uin
 }
 
 // ALIGNED: K is a multiple of 128 and at least 512 and the scales are 4-byte aligned. Their rows are then copied
-// straight to LDS like the codes; else they pass through registers, whose wait (the compiler's, for every
-// copy in flight) costs a stall in each group of four steps.
+// straight to LDS like the codes; else they pass through registers, where the compiler's wait for them is one
+// for every copy in flight.
 template <int MODE, int WT, int WC, int MT, int NT, bool ALIGNED>
 __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expert, int row0, int nrows, int cg,
                                           uint8_t* lds) {
@@ -300,22 +299,22 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     else col = min(cg * S::TC + j, a.N - 1);
     return scales ? ws + col * nblk : wq + col * (a.K / 2);
   };
-  const uint8_t* src[S::LPS];
+  const uint8_t* src[S::LPP];
 #pragma unroll
-  for (int i = 0; i < S::LPS; ++i) src[i] = source(16 * (wv + 4 * i) + (lane >> 2), false);
+  for (int i = 0; i < S::LPP; ++i) src[i] = source(8 * (wv + 4 * i) + (lane >> 3), false);
   const uint8_t* ssrc[S::SPT];
 #pragma unroll
   for (int i = 0; i < S::SPT; ++i) {
     if constexpr (ALIGNED) ssrc[i] = source(64 * min(wv + 4 * i, (S::TR + S::TC) / 64 - 1) + lane, true);
     else ssrc[i] = nblk >= 16 ? source(min(tid + 256 * i, S::TR + S::TC - 1), true) : a.wq;
   }
-  const int chunk = (lane & 3) ^ swizzle(lane >> 2);
+  const int chunk = (lane & 7) ^ swizzle(8 * (wv & 1) + (lane >> 3));
 
-  auto issue = [&](int ks, int i) {              // one of a wavefront's LPS copies (16 rows) of step ks
-    const int blk = min(4 * ks + chunk, nblk - 1);
+  auto issue = [&](int pair, int i) {            // one of a wavefront's LPP copies (8 rows) of a pair of steps
+    const int blk = min(8 * pair + chunk, nblk - 1);
     __builtin_amdgcn_global_load_lds(
         (const void __attribute__((address_space(1)))*)(src[i] + 16 * blk),
-        (void __attribute__((address_space(3)))*)(lds + (ks % kDepth) * S::kSlot + (wv + 4 * i) * 1024), 16, 0, 0);
+        (void __attribute__((address_space(3)))*)(lds + (pair & 1) * S::kSlot + (wv + 4 * i) * 1024), 16, 0, 0);
   };
   // Scales of steps 4 g .. 4 g + 3: bytes 16 g .. of each row. The last group's load starts where it ends with
   // the row and is shifted when it is stored; rows shorter than 16 bytes have one
@@ -326,7 +325,7 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     for (int i = 0; i < S::SPT; ++i)
       __builtin_amdgcn_global_load_lds(
           (const void __attribute__((address_space(1)))*)(ssrc[i] + from),
-          (void __attribute__((address_space(3)))*)(lds + kDepth * S::kSlot + (g & 1) * S::kScales +
+          (void __attribute__((address_space(3)))*)(lds + 2 * S::kSlot + (g & 1) * S::kScales +
                                                     min(wv + 4 * i, (S::TR + S::TC) / 64 - 1) * 1024),
           16, 0, 0);
   };
@@ -337,7 +336,7 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     for (int i = 0; i < S::SPT; ++i) __builtin_memcpy(&sreg[i], ssrc[i] + from, 16);
   };
   auto store_scales = [&](int g) {               // no branches: the loop body stays one block
-    uint8_t* buf = lds + kDepth * S::kSlot + (g & 1) * S::kScales;
+    uint8_t* buf = lds + 2 * S::kSlot + (g & 1) * S::kScales;
     const int by = max(16 * g - (nblk - 16), 0);   // bytes to shift out: 8 and 4 by masks, the rest by alignbyte
     uint32_t keep[2] = {by & 8 ? 0u : ~0u, by & 4 ? 0u : ~0u};
     asm("" : "+v"(keep[0]), "+v"(keep[1]));      // opaque: selects on a known condition become branches
@@ -363,7 +362,7 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
       store_scales(0);
       return;
     }
-    uint8_t* buf = lds + kDepth * S::kSlot;
+    uint8_t* buf = lds + 2 * S::kSlot;
     for (int i = tid; i < S::TR + S::TC; i += 256) {
       const uint8_t* p = source(i, true);
       for (int b = 0; b < 16; ++b) buf[16 * i + b] = b < nblk ? p[b] : 0;
@@ -374,21 +373,23 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     i4v x[MT], w[NT];
   };
   const int place = swizzle(r32);
-  const int lane0 = 64 * r32 + 16 * ((2 * h) ^ place), lane1 = 64 * r32 + 16 * ((2 * h + 1) ^ place);
+  int lane_at[4];                                // chunk 4 (ks & 1) + 2 h + s of a row, by 2 (ks & 1) + s
+#pragma unroll
+  for (int i = 0; i < 4; ++i) lane_at[i] = 128 * r32 + 16 * ((4 * (i >> 1) + 2 * h + (i & 1)) ^ place);
   // Piece p of MT + NT reads one fragment of sub-step s of step ks (and, with SCALES, its scales): the columns
   // first, which every matrix instruction of the first row needs.
   int xs[MT], ws4[NT], nx[MT], nw[NT];
   auto read_piece = [&](int ks, int s, int p, Frags& f, bool scales) {
-    const uint8_t* slot = lds + (ks % kDepth) * S::kSlot + (s ? lane1 : lane0);
+    const uint8_t* slot = lds + ((ks >> 1) & 1) * S::kSlot + lane_at[2 * (ks & 1) + s];
     // ALIGNED: the last group's bytes start where they end with the row
     const int at = ALIGNED ? min(4 * ks - min(16 * (ks >> 2), nblk - 16), 12) : 4 * (ks & 3);
-    const uint8_t* sc = lds + kDepth * S::kSlot + ((ks >> 2) & 1) * S::kScales + 16 * r32 + at + 2 * h;
+    const uint8_t* sc = lds + 2 * S::kSlot + ((ks >> 2) & 1) * S::kScales + 16 * r32 + at + 2 * h;
     if (p < NT) {
-      f.w[p] = *reinterpret_cast<const i4v*>(slot + 64 * S::TR + 2048 * (wc * NT + p));
+      f.w[p] = *reinterpret_cast<const i4v*>(slot + 128 * S::TR + 4096 * (wc * NT + p));
       if (scales) nw[p] = *reinterpret_cast<const uint16_t*>(sc + 16 * S::TR + 512 * (wc * NT + p));
     } else {
       const int m = p - NT;
-      f.x[m] = *reinterpret_cast<const i4v*>(slot + 2048 * (wt * MT + m));
+      f.x[m] = *reinterpret_cast<const i4v*>(slot + 4096 * (wt * MT + m));
       if (scales) nx[m] = *reinterpret_cast<const uint16_t*>(sc + 512 * (wt * MT + m));
     }
   };
@@ -402,10 +403,10 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
   if constexpr (ALIGNED) copy_scales(0);
   else first_scales();
 #pragma unroll
-  for (int d = 0; d < kDepth; ++d)
+  for (int d = 0; d < 2; ++d)
 #pragma unroll
-    for (int i = 0; i < S::LPS; ++i) issue(d, i);
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::LPS * (kDepth - 1)) : "memory");
+    for (int i = 0; i < S::LPP; ++i) issue(d, i);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::LPP) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   Frags f0, f1;
@@ -438,22 +439,23 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
       acc[j / NT][j % NT] = mma32<0>(f0.w[j % NT], ws4[j % NT], f0.x[j / NT], xs[j / NT], acc[j / NT][j % NT]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    // Step ks + 1 has landed: the copies of steps ks + 2 and ks + 3 may still be in flight, and the scales'
-    // that were issued after those of ks + 1 (steps 0 and 1 of a group; other loads among them would only
-    // make the wait stricter), and this wavefront's LDS accesses are done. Behind the barrier that holds for
-    // all four wavefronts: the slot of step ks is free. The next group's scales are read from the middle of
-    // step 3 on: step 2's wait covers them.
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::LPS * (kDepth - 2) + (ALIGNED && PHASE < 2 ? S::SPT : 0))
-                 : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    // Second step of a pair: the next pair has landed (the only newer copies are those of the scales, issued
+    // in step 0 of the group; step 3's wait covers them) and this wavefront's LDS accesses are done. Behind
+    // the barrier that holds for all four wavefronts: this pair's slot is free.
+    if constexpr (PHASE & 1) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(ALIGNED && PHASE == 1 ? S::SPT : 0) : "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    }
 #pragma unroll
     for (int j = 0; j < MM; ++j) {
       constexpr int per = (RD + MM - 1) / MM;
 #pragma unroll
       for (int p = j * per; p < (j + 1) * per && p < RD; ++p) read_piece(ks + 1, 0, p, f0, true);
+      if constexpr (PHASE & 1) {
 #pragma unroll
-      for (int i = j * S::LPS / MM; i < (j + 1) * S::LPS / MM; ++i) issue(ks + kDepth, i);
+        for (int i = j * S::LPP / MM; i < (j + 1) * S::LPP / MM; ++i) issue((ks >> 1) + 2, i);
+      }
       __builtin_amdgcn_sched_barrier(0);
       acc[j / NT][j % NT] = mma32<1>(f1.w[j % NT], ws4[j % NT], f1.x[j / NT], xs[j / NT], acc[j / NT][j % NT]);
       __builtin_amdgcn_sched_barrier(0);
