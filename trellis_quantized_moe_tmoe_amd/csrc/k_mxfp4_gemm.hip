@@ -547,6 +547,22 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_tile_dense(Mxfp4GemmArgs a, in
   tile_body<MODE, WT, WC, MT, NT, ALIGNED>(a, 0, row0, min(S::TR, a.rows - row0), ct, lds);
 }
 
+// Grouped: tiles of up to 128 rows of one expert by 256 columns (first product: 128 gate and 128 up). A tile's
+// column blocks go to one XCD, which then reads its rows once. Tiles of at most 64 rows run with half the
+// row fragments; the tile list holds them last.
+template <int MODE, bool ALIGNED>
+__global__ __launch_bounds__(256, 1) void k_mxfp4_tile_grouped(Mxfp4GemmArgs a, int col_tiles) {
+  using S = Tile<MODE, 1, 4, 4, 2>;
+  __shared__ __align__(16) uint8_t lds[S::kLds];
+  const int i = blockIdx.x / 8;
+  const int tile = i / col_tiles * 8 + blockIdx.x % 8, ct = i % col_tiles;
+  if (tile >= *a.num_gtiles) return;
+  const int4 t = a.gtiles[tile];
+  const long long expert = t.x & 0xffffff;
+  if (t.z > 64) tile_body<MODE, 1, 4, 4, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
+  else tile_body<MODE, 1, 4, 2, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
+}
+
 // y_t = sum over j ascending of w[t][j] * v[slot of (t, j)], four columns a thread.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_mxfp4_combine(Mxfp4CombineArgs a) {
@@ -569,7 +585,9 @@ __global__ __launch_bounds__(256) void k_mxfp4_combine(Mxfp4CombineArgs a) {
 
 }  // namespace
 
-int mxfp4_tile_rows(long long routes, int experts) { return routes <= 4LL * experts ? 16 : 64; }
+// Rows of a tile of the expert layer: 16 while experts hold a few rows each (straight from global memory), else
+// 128 (through LDS).
+int mxfp4_tile_rows(long long routes, int experts) { return routes <= 12LL * experts ? 16 : 128; }
 
 template <int MODE>
 void launch_direct(const Mxfp4GemmArgs& a, bool small, int tiles, hipStream_t s) {
@@ -587,7 +605,7 @@ void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s) {
   const int rt = (a.rows + 255) / 256, ct = (a.N + 255) / 256;
   if (rt * ct >= 64) {
     const dim3 g((rt * ct + 7) / 8 * 8);
-    auto go = [&](auto bf, auto al) {
+    auto go = [&](auto bf, auto al) {   // bf16 result, aligned scales
       constexpr int MODE = decltype(bf)::value ? kDenseBf16 : kDenseF32;
       hipLaunchKernelGGL((k_mxfp4_tile_dense<MODE, 2, 2, 4, 4, decltype(al)::value>), g, dim3(256), 0, s, a, rt, ct);
     };
@@ -602,13 +620,20 @@ void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s) {
   else launch_direct<kDenseF32>(a, small, tiles, s);
 }
 
-void launch_mxfp4_fc1(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) {
-  launch_direct<kFc1>(a, tile_rows == 16, a.max_gtiles, s);
+template <int MODE>
+void launch_grouped(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) {
+  if (tile_rows == 16) {
+    launch_direct<MODE>(a, true, a.max_gtiles, s);
+    return;
+  }
+  const int ct = (a.N + 255) / 256;
+  const dim3 g((a.max_gtiles + 7) / 8 * 8 * ct);
+  if (scales_aligned(a)) hipLaunchKernelGGL((k_mxfp4_tile_grouped<MODE, true>), g, dim3(256), 0, s, a, ct);
+  else hipLaunchKernelGGL((k_mxfp4_tile_grouped<MODE, false>), g, dim3(256), 0, s, a, ct);
 }
 
-void launch_mxfp4_fc2(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) {
-  launch_direct<kFc2>(a, tile_rows == 16, a.max_gtiles, s);
-}
+void launch_mxfp4_fc1(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) { launch_grouped<kFc1>(a, tile_rows, s); }
+void launch_mxfp4_fc2(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) { launch_grouped<kFc2>(a, tile_rows, s); }
 
 void launch_mxfp4_combine(const Mxfp4CombineArgs& a, int y_dtype, hipStream_t s) {
   const long long n = static_cast<long long>(a.tokens) * (a.H / 4);
