@@ -551,16 +551,16 @@ __global__ __launch_bounds__(256, 1) void k_mxfp4_tile_dense(Mxfp4GemmArgs a, in
 // column blocks go to one XCD, which then reads its rows once. Tiles of at most 64 rows run with half the
 // row fragments; the tile list holds them last.
 template <int MODE, bool ALIGNED>
-__global__ __launch_bounds__(256, 1) void k_mxfp4_tile_grouped(Mxfp4GemmArgs a, int col_tiles) {
-  using S = Tile<MODE, 1, 4, 4, 2>;
+__global__ __launch_bounds__(256, 2) void k_mxfp4_tile_grouped(Mxfp4GemmArgs a, int col_tiles) {
+  using S = Tile<MODE, 2, 2, 2, 2>;
   __shared__ __align__(16) uint8_t lds[S::kLds];
   const int i = blockIdx.x / 8;
   const int tile = i / col_tiles * 8 + blockIdx.x % 8, ct = i % col_tiles;
   if (tile >= *a.num_gtiles) return;
   const int4 t = a.gtiles[tile];
   const long long expert = t.x & 0xffffff;
-  if (t.z > 64) tile_body<MODE, 1, 4, 4, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
-  else tile_body<MODE, 1, 4, 2, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
+  if (t.z > 64) tile_body<MODE, 2, 2, 2, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
+  else tile_body<MODE, 2, 2, 1, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
 }
 
 // y_t = sum over j ascending of w[t][j] * v[slot of (t, j)], four columns a thread.
@@ -626,7 +626,7 @@ void launch_grouped(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) {
     launch_direct<MODE>(a, true, a.max_gtiles, s);
     return;
   }
-  const int ct = (a.N + 255) / 256;
+  const int ct = (a.N + 127) / 128;
   const dim3 g((a.max_gtiles + 7) / 8 * 8 * ct);
   if (scales_aligned(a)) hipLaunchKernelGGL((k_mxfp4_tile_grouped<MODE, true>), g, dim3(256), 0, s, a, ct);
   else hipLaunchKernelGGL((k_mxfp4_tile_grouped<MODE, false>), g, dim3(256), 0, s, a, ct);
