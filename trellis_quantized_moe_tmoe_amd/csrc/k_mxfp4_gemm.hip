@@ -23,24 +23,6 @@ __device__ __forceinline__ f4 mma(i4v w, int ws, i4v x, int xs, f4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, ws, 0, xs);
 }
 
-struct Frag {
-  i4v q;
-  int s;
-};
-
-// Block `blk` of a row; blocks past the row (the tail of a K that is no multiple of 128) are zeros.
-__device__ __forceinline__ Frag load_block(const uint8_t* q, const uint8_t* s, int blk, int nblk) {
-  Frag f;
-  if (blk < nblk) {
-    f.q = reinterpret_cast<const i4v*>(q)[blk];
-    f.s = s[blk];
-  } else {
-    f.q = i4v{0, 0, 0, 0};
-    f.s = 127;
-  }
-  return f;
-}
-
 // Four neighbouring columns col.. of a row of N, at element `at` of y; columns past N are dropped. QUADS: N
 // is a multiple of four, so a quad is whole and aligned.
 template <bool BF16, bool QUADS>
@@ -98,23 +80,26 @@ __device__ __forceinline__ void store_swiglu(const f4 (&g)[2], const f4 (&u)[2],
   }
 }
 
-// A wavefront computes 16 MT rows by 16 NT columns straight from global memory. KW = 4: the workgroup's
-// wavefronts share one tile and take every fourth 128-deep step each, joined in LDS in a fixed order;
-// KW = 1: they take neighbouring column groups.
-template <int MODE, int MT, int NT, int KW>
-__global__ __launch_bounds__(256) void k_mxfp4_direct(Mxfp4GemmArgs a) {
-  static_assert(MODE != kFc1 || NT == 4, "first product: two gate and two up fragments");
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// Few rows: a workgroup of KW wavefronts computes 16 MT rows by 16 NT columns straight from global memory,
+// each wavefront every KW-th 128-deep step, their sums joined in LDS in a fixed order. What bounds it is the
+// latency of a wavefront's loads, so they are issued AH steps at a time (the weights first: they do not wait
+// for the tile's routes) and, with TWO, the next batch before the products of the one before; the expert
+// layer's products have many workgroups a CU instead, and few registers keep them there. Blocks past K repeat
+// the last one with the scale 2^-127 on both sides (see the tiles below).
+template <int MODE, int MT, int NT, int KW, int AH, bool TWO>
+__global__ __launch_bounds__(64 * KW) void k_mxfp4_rows(Mxfp4GemmArgs a) {
+  static_assert(MODE != kFc1 || (NT == 4 && MT == 1), "first product: two gate and two up fragments");
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   // workgroups in x only (a tile's column groups next to each other): y and z are limited to 65535
   const int ngroups = MODE == kFc1 ? a.N / 64 : (a.N + 16 * NT - 1) / (16 * NT);
-  const int nwg = KW == 1 ? (ngroups + 3) / 4 : ngroups;
-  const int tile = blockIdx.x / nwg, wg = blockIdx.x % nwg;
+  const int tile = blockIdx.x / ngroups, group = blockIdx.x % ngroups;
   int row0, nrows;
   long long expert = 0;
   if constexpr (MODE == kFc1 || MODE == kFc2) {
-    if (tile >= *a.num_gtiles) return;
-    const int4 t = a.gtiles[tile];
+    const int count = *a.num_gtiles;
+    const int4 t = a.gtiles[tile];               // tile < max_gtiles: inside the list, also past its count
+    if (tile >= count) return;
     expert = t.x & 0xffffff;
     row0 = t.y;
     nrows = t.z;
@@ -122,20 +107,11 @@ __global__ __launch_bounds__(256) void k_mxfp4_direct(Mxfp4GemmArgs a) {
     row0 = tile * 16 * MT;
     nrows = min(16 * MT, a.rows - row0);
   }
-  const int group = KW == 1 ? wg * 4 + wv : wg;
-  if (KW == 1 && group >= ngroups) return;
   const int nblk = a.K / 32, steps = (nblk + 3) / 4;
   const uint8_t* wq = a.wq + expert * a.N * (a.K / 2);
   const uint8_t* ws = a.ws + expert * a.N * nblk;
 
-  const uint8_t *xq[MT], *xs[MT], *pq[NT], *ps[NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    long long row = row0 + min(16 * m + r, nrows - 1);
-    if constexpr (MODE == kFc1) row = a.sorted[row] / a.top_k;
-    xq[m] = a.xq + row * (a.K / 2);
-    xs[m] = a.xs + row * nblk;
-  }
+  const uint8_t *pq[NT], *ps[NT], *xq[MT], *xs[MT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     long long col;
@@ -144,56 +120,115 @@ __global__ __launch_bounds__(256) void k_mxfp4_direct(Mxfp4GemmArgs a) {
     pq[n] = wq + col * (a.K / 2);
     ps[n] = ws + col * nblk;
   }
+  struct Batch {
+    i4v w[AH][NT], x[AH][MT];
+    int ws[AH][NT], xs[AH][MT];
+  };
+  auto load_w = [&](int st, Batch& b) {
+#pragma unroll
+    for (int u = 0; u < AH; ++u) {
+      const int blk = 4 * (st + u * KW) + q, at = min(blk, nblk - 1);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        b.w[u][n] = reinterpret_cast<const i4v*>(pq[n])[at];
+        b.ws[u][n] = ps[n][at];
+      }
+    }
+  };
+  auto load_x = [&](int st, Batch& b) {
+#pragma unroll
+    for (int u = 0; u < AH; ++u) {
+      const int blk = 4 * (st + u * KW) + q, at = min(blk, nblk - 1);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        b.x[u][m] = reinterpret_cast<const i4v*>(xq[m])[at];
+        b.xs[u][m] = xs[m][at];
+      }
+    }
+  };
+  Batch b0, b1;
+  load_w(wv, b0);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    long long row = row0 + min(16 * m + r, nrows - 1);
+    if constexpr (MODE == kFc1) row = a.sorted[row] / a.top_k;
+    xq[m] = a.xq + row * (a.K / 2);
+    xs[m] = a.xs + row * nblk;
+  }
+  load_x(wv, b0);
   f4 acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = f4{0, 0, 0, 0};
-  for (int st = KW == 1 ? 0 : wv; st < steps; st += KW) {
-    const int blk = 4 * st + q;
-    Frag x[MT], w[NT];
+  auto multiply = [&](int st, const Batch& b) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) w[n] = load_block(pq[n], ps[n], blk, nblk);
+    for (int u = 0; u < AH; ++u) {
+      const bool in = 4 * (st + u * KW) + q < nblk;
+      int sx[MT], sw[NT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) x[m] = load_block(xq[m], xs[m], blk, nblk);
+      for (int m = 0; m < MT; ++m) sx[m] = in ? b.xs[u][m] : 0;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n] = mma(w[n].q, w[n].s, x[m].q, x[m].s, acc[m][n]);
-  }
-  if constexpr (KW > 1) {
-    __shared__ f4 part[KW - 1][MT * NT][64];
-    if (wv > 0) {
+      for (int n = 0; n < NT; ++n) sw[n] = in ? b.ws[u][n] : 0;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) part[wv - 1][m * NT + n][lane] = acc[m][n];
+        for (int n = 0; n < NT; ++n) acc[m][n] = mma(b.w[u][n], sw[n], b.x[u][m], sx[m], acc[m][n]);
     }
-    __syncthreads();
-    if (wv > 0) return;
-#pragma unroll
-    for (int p = 0; p < KW - 1; ++p)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n] += part[p][m * NT + n][lane];
-  }
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const bool live = 16 * m + r < nrows;
-    const long long row = row0 + 16 * m + r;
-    if constexpr (MODE == kFc1) {
-      const f4 g[2] = {acc[m][0], acc[m][1]}, u[2] = {acc[m][2], acc[m][3]};
-      const int inter = a.N / 2;
-      store_swiglu(g, u, a.bq + row * (inter / 2) + 16 * group, a.bs + row * (inter / 32) + group, lane, live);
-    } else {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int col = 16 * NT * group + 16 * n + 4 * q;
-        if (!live) continue;
-        if (a.N % 4 == 0) store4<MODE == kDenseBf16, true>(a.y, row * a.N + col, col, a.N, acc[m][n]);
-        else store4<MODE == kDenseBf16, false>(a.y, row * a.N + col, col, a.N, acc[m][n]);
+  };
+  constexpr int kStride = KW * AH;
+  int st = wv;
+  if constexpr (TWO) {
+    for (; st + kStride < steps; st += 2 * kStride) {
+      load_w(st + kStride, b1);
+      load_x(st + kStride, b1);
+      multiply(st, b0);
+      if (st + 2 * kStride < steps) {
+        load_w(st + 2 * kStride, b0);
+        load_x(st + 2 * kStride, b0);
       }
+      multiply(st + kStride, b1);
+    }
+    if (st < steps) multiply(st, b0);
+  } else {
+    while (st < steps) {
+      multiply(st, b0);
+      st += kStride;
+      if (st < steps) {
+        load_w(st, b0);
+        load_x(st, b0);
+      }
+    }
+  }
+
+  // join: fragment f of MT * NT belongs to wavefront f % KW (first product: all of them to wavefront 0)
+  __shared__ f4 part[KW][MT * NT][64];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) part[wv][m * NT + n][lane] = acc[m][n];
+  __syncthreads();
+  auto total = [&](int f) {
+    f4 s = part[0][f][lane];
+#pragma unroll
+    for (int p = 1; p < KW; ++p) s += part[p][f][lane];
+    return s;
+  };
+  if constexpr (MODE == kFc1) {
+    if (wv > 0) return;
+    const f4 g[2] = {total(0), total(1)}, u[2] = {total(2), total(3)};
+    const int inter = a.N / 2;
+    const long long row = row0 + r;
+    store_swiglu(g, u, a.bq + row * (inter / 2) + 16 * group, a.bs + row * (inter / 32) + group, lane, r < nrows);
+  } else {
+    for (int f = wv; f < MT * NT; f += KW) {
+      const f4 s = total(f);
+      const int m = f / NT, n = f % NT;
+      const int col = 16 * NT * group + 16 * n + 4 * q;
+      const long long at = static_cast<long long>(row0 + 16 * m + r) * a.N + col;
+      if (16 * m + r >= nrows) continue;
+      if (a.N % 4 == 0) store4<MODE == kDenseBf16, true>(a.y, at, col, a.N, s);
+      else store4<MODE == kDenseBf16, false>(a.y, at, col, a.N, s);
     }
   }
 }
@@ -589,41 +624,45 @@ __global__ __launch_bounds__(256) void k_mxfp4_combine(Mxfp4CombineArgs a) {
 // 128 (through LDS).
 int mxfp4_tile_rows(long long routes, int experts) { return routes <= 12LL * experts ? 16 : 128; }
 
-template <int MODE>
-void launch_direct(const Mxfp4GemmArgs& a, bool small, int tiles, hipStream_t s) {
-  const int cols = MODE == kFc1 ? a.N / 64 : (a.N + 63) / 64;
-  if (small) hipLaunchKernelGGL((k_mxfp4_direct<MODE, 1, 4, 4>), dim3(cols * tiles), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_mxfp4_direct<MODE, 4, 4, 1>), dim3((cols + 3) / 4 * tiles), dim3(256), 0, s, a);
-}
-
 bool scales_aligned(const Mxfp4GemmArgs& a) {
   return a.K % 128 == 0 && a.K >= 512 &&
          ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
 }
 
-void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s) {
+template <int MODE>
+void launch_dense(const Mxfp4GemmArgs& a, hipStream_t s) {
   const int rt = (a.rows + 255) / 256, ct = (a.N + 255) / 256;
   if (rt * ct >= 64) {
     const dim3 g((rt * ct + 7) / 8 * 8);
-    auto go = [&](auto bf, auto al) {   // bf16 result, aligned scales
-      constexpr int MODE = decltype(bf)::value ? kDenseBf16 : kDenseF32;
-      hipLaunchKernelGGL((k_mxfp4_tile_dense<MODE, 2, 2, 4, 4, decltype(al)::value>), g, dim3(256), 0, s, a, rt, ct);
-    };
-    const bool al = scales_aligned(a);
-    if (y_dtype == TMOE_BF16) al ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
-    else al ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+    if (scales_aligned(a)) hipLaunchKernelGGL((k_mxfp4_tile_dense<MODE, 2, 2, 4, 4, true>), g, dim3(256), 0, s, a, rt, ct);
+    else hipLaunchKernelGGL((k_mxfp4_tile_dense<MODE, 2, 2, 4, 4, false>), g, dim3(256), 0, s, a, rt, ct);
     return;
   }
-  const bool small = a.rows <= 16;
-  const int tiles = small ? 1 : (a.rows + 63) / 64;
-  if (y_dtype == TMOE_BF16) launch_direct<kDenseBf16>(a, small, tiles, s);
-  else launch_direct<kDenseF32>(a, small, tiles, s);
+  auto rows = [&](auto mt, auto nt, auto ah) {
+    constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, AH = decltype(ah)::value;
+    const int groups = (a.N + 16 * NT - 1) / (16 * NT), tiles = (a.rows + 16 * MT - 1) / (16 * MT);
+    hipLaunchKernelGGL((k_mxfp4_rows<MODE, MT, NT, 8, AH, true>), dim3(groups * tiles), dim3(512), 0, s, a);
+  };
+  std::integral_constant<int, 1> one;
+  std::integral_constant<int, 2> two;
+  std::integral_constant<int, 4> four;
+  if (a.rows <= 16) rows(one, one, four);
+  else if (a.rows <= 32) rows(two, one, two);
+  else if (a.rows <= 64) rows(four, one, two);
+  else rows(four, two, one);
+}
+
+void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s) {
+  if (y_dtype == TMOE_BF16) launch_dense<kDenseBf16>(a, s);
+  else launch_dense<kDenseF32>(a, s);
 }
 
 template <int MODE>
 void launch_grouped(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) {
   if (tile_rows == 16) {
-    launch_direct<MODE>(a, true, a.max_gtiles, s);
+    const dim3 g((a.N + 63) / 64 * a.max_gtiles);
+    if (a.K <= 512) hipLaunchKernelGGL((k_mxfp4_rows<MODE, 1, 4, 4, 1, false>), g, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_mxfp4_rows<MODE, 1, 4, 4, 2, false>), g, dim3(256), 0, s, a);
     return;
   }
   const int ct = (a.N + 127) / 128;
