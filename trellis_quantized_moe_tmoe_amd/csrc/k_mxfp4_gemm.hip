@@ -15,7 +15,7 @@ namespace {
 typedef int i4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 
-enum { kDenseF32 = 0, kDenseBf16 = 1, kFc1 = 2, kFc2 = 3 };
+enum { kDenseF32 = 0, kDenseBf16 = 1, kFc1 = 2, kFc2 = 3, kFc1Few = 4, kFc2Few = 5 };
 
 __device__ __forceinline__ f4 mma(i4v w, int ws, i4v x, int xs, f4 c) {
   const i8v a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -86,17 +86,48 @@ __device__ __forceinline__ void store_swiglu(const f4 (&g)[2], const f4 (&u)[2],
 // for the tile's routes) and, with TWO, the next batch before the products of the one before; the expert
 // layer's products have many workgroups a CU instead, and few registers keep them there. Blocks past K repeat
 // the last one with the scale 2^-127 on both sides (see the tiles below).
+//
+// kFc1Few, kFc2Few (up to kFewRoutesMax routes): there is no tile list. A workgroup stands for a route, finds
+// the routes of that route's expert itself, one id a thread, and goes on if it is the 1st, 17th, ... of them,
+// with the 16 from there on; slots are the routes. That saves the route map's launch (5.8 us of 35 at T = 16,
+// k = 8, E = 96, H = 1024, I = 512).
 template <int MODE, int MT, int NT, int KW, int AH, bool TWO>
-__global__ __launch_bounds__(64 * KW) void k_mxfp4_rows(Mxfp4GemmArgs a) {
-  static_assert(MODE != kFc1 || (NT == 4 && MT == 1), "first product: two gate and two up fragments");
+__global__ __launch_bounds__(64 * KW, TWO ? 2 : 5) void k_mxfp4_rows(Mxfp4GemmArgs a) {
+  constexpr bool FC1 = MODE == kFc1 || MODE == kFc1Few, FEW = MODE == kFc1Few || MODE == kFc2Few;
+  static_assert(!FC1 || (NT == 4 && MT == 1), "first product: two gate and two up fragments");
+  static_assert(!FEW || (KW * 64 == kFewRoutesMax && MT == 1), "one id a thread, tiles of 16 routes");
+  __shared__ int list[FEW ? kFewRoutesMax : 1];
+  __shared__ int first[FEW ? KW : 1], my_rank;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   // workgroups in x only (a tile's column groups next to each other): y and z are limited to 65535
-  const int ngroups = MODE == kFc1 ? a.N / 64 : (a.N + 16 * NT - 1) / (16 * NT);
+  const int ngroups = FC1 ? a.N / 64 : (a.N + 16 * NT - 1) / (16 * NT);
   const int tile = blockIdx.x / ngroups, group = blockIdx.x % ngroups;
-  int row0, nrows;
+  int row0 = 0, nrows;
   long long expert = 0;
-  if constexpr (MODE == kFc1 || MODE == kFc2) {
+  if constexpr (FEW) {
+    const int tid = threadIdx.x;
+    long long id = -1;
+    if (tid < a.routes) id = a.ids64 ? static_cast<const long long*>(a.ids)[tid] : static_cast<const int*>(a.ids)[tid];
+    expert = a.ids64 ? static_cast<const long long*>(a.ids)[tile] : static_cast<const int*>(a.ids)[tile];
+    if (expert < 0 || expert >= a.experts) return;           // the same for the whole workgroup
+    const unsigned long long mine = __ballot(id == expert);
+    if (lane == 0) first[wv] = __popcll(mine);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int p = 0; p < KW; ++p) {
+      if (p < wv) before += first[p];
+      all += first[p];
+    }
+    const int rank = before + __popcll(mine & ((1ull << lane) - 1));
+    if (id == expert) list[rank] = tid;
+    if (tid == tile) my_rank = rank;
+    __syncthreads();
+    row0 = my_rank;                              // a tile's rows: list[row0 ..]
+    nrows = min(16, all - row0);
+    if (row0 % 16 != 0) return;
+  } else if constexpr (MODE == kFc1 || MODE == kFc2) {
     const int count = *a.num_gtiles;
     const int4 t = a.gtiles[tile];               // tile < max_gtiles: inside the list, also past its count
     if (tile >= count) return;
@@ -115,7 +146,7 @@ __global__ __launch_bounds__(64 * KW) void k_mxfp4_rows(Mxfp4GemmArgs a) {
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     long long col;
-    if constexpr (MODE == kFc1) col = (n >> 1) * (a.N / 2) + 32 * group + 16 * (n & 1) + r;
+    if constexpr (FC1) col = (n >> 1) * (a.N / 2) + 32 * group + 16 * (n & 1) + r;
     else col = min(16 * NT * group + 16 * n + r, a.N - 1);
     pq[n] = wq + col * (a.K / 2);
     ps[n] = ws + col * nblk;
@@ -146,12 +177,17 @@ __global__ __launch_bounds__(64 * KW) void k_mxfp4_rows(Mxfp4GemmArgs a) {
       }
     }
   };
+  __shared__ f4 part[KW][MT * NT][64];
+  constexpr int kStride = KW * AH;
   Batch b0, b1;
   load_w(wv, b0);
+  long long slot[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    long long row = row0 + min(16 * m + r, nrows - 1);
+    slot[m] = FEW ? list[row0 + min(r, nrows - 1)] : row0 + min(16 * m + r, nrows - 1);
+    long long row = slot[m];
     if constexpr (MODE == kFc1) row = a.sorted[row] / a.top_k;
+    if constexpr (MODE == kFc1Few) row = row / a.top_k;
     xq[m] = a.xq + row * (a.K / 2);
     xs[m] = a.xs + row * nblk;
   }
@@ -176,7 +212,6 @@ __global__ __launch_bounds__(64 * KW) void k_mxfp4_rows(Mxfp4GemmArgs a) {
         for (int n = 0; n < NT; ++n) acc[m][n] = mma(b.w[u][n], sw[n], b.x[u][m], sx[m], acc[m][n]);
     }
   };
-  constexpr int kStride = KW * AH;
   int st = wv;
   if constexpr (TWO) {
     for (; st + kStride < steps; st += 2 * kStride) {
@@ -202,7 +237,6 @@ __global__ __launch_bounds__(64 * KW) void k_mxfp4_rows(Mxfp4GemmArgs a) {
   }
 
   // join: fragment f of MT * NT belongs to wavefront f % KW (first product: all of them to wavefront 0)
-  __shared__ f4 part[KW][MT * NT][64];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -214,18 +248,19 @@ __global__ __launch_bounds__(64 * KW) void k_mxfp4_rows(Mxfp4GemmArgs a) {
     for (int p = 1; p < KW; ++p) s += part[p][f][lane];
     return s;
   };
-  if constexpr (MODE == kFc1) {
-    if (wv > 0) return;
-    const f4 g[2] = {total(0), total(1)}, u[2] = {total(2), total(3)};
-    const int inter = a.N / 2;
-    const long long row = row0 + r;
-    store_swiglu(g, u, a.bq + row * (inter / 2) + 16 * group, a.bs + row * (inter / 32) + group, lane, r < nrows);
+  if constexpr (FC1) {
+    if (wv == 0) {
+      const f4 g[2] = {total(0), total(1)}, u[2] = {total(2), total(3)};
+      const int inter = a.N / 2;
+      store_swiglu(g, u, a.bq + slot[0] * (inter / 2) + 16 * group, a.bs + slot[0] * (inter / 32) + group, lane,
+                   r < nrows);
+    }
   } else {
     for (int f = wv; f < MT * NT; f += KW) {
       const f4 s = total(f);
       const int m = f / NT, n = f % NT;
       const int col = 16 * NT * group + 16 * n + 4 * q;
-      const long long at = static_cast<long long>(row0 + 16 * m + r) * a.N + col;
+      const long long at = (FEW ? slot[0] : row0 + 16 * m + r) * a.N + col;
       if (16 * m + r >= nrows) continue;
       if (a.N % 4 == 0) store4<MODE == kDenseBf16, true>(a.y, at, col, a.N, s);
       else store4<MODE == kDenseBf16, false>(a.y, at, col, a.N, s);
@@ -598,7 +633,8 @@ __global__ __launch_bounds__(256, 2) void k_mxfp4_tile_grouped(Mxfp4GemmArgs a, 
   else tile_body<MODE, 2, 2, 1, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
 }
 
-// y_t = sum over j ascending of w[t][j] * v[slot of (t, j)], four columns a thread.
+// y_t = sum over j ascending of w[t][j] * v[slot of (t, j)], four columns a thread; eight rows' loads in
+// flight (one after the other: 6.5 us at T = 16, k = 8).
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_mxfp4_combine(Mxfp4CombineArgs a) {
   const int quads = a.H / 4;
@@ -607,10 +643,28 @@ __global__ __launch_bounds__(256) void k_mxfp4_combine(Mxfp4CombineArgs a) {
   const long long t = i / quads;
   const int c = static_cast<int>(i - t * quads);
   f4 s = {0, 0, 0, 0};
-  for (int j = 0; j < a.top_k; ++j) {
-    const int slot = a.route_slot[t * a.top_k + j];
-    if (slot < 0) continue;
-    s += a.w[t * a.top_k + j] * reinterpret_cast<const f4*>(a.v + static_cast<long long>(slot) * a.H)[c];
+  for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+    long long slot[8];
+    float w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const long long r = t * a.top_k + min(j0 + u, a.top_k - 1);
+      w[u] = a.w[r];
+      if (a.route_slot) {
+        slot[u] = a.route_slot[r];
+      } else {
+        const long long id = a.ids64 ? static_cast<const long long*>(a.ids)[r] : static_cast<const int*>(a.ids)[r];
+        slot[u] = id >= 0 && id < a.experts ? r : -1;
+      }
+      if (j0 + u >= a.top_k) slot[u] = -1;
+    }
+    f4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (slot[u] >= 0) v[u] = reinterpret_cast<const f4*>(a.v + slot[u] * a.H)[c];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (slot[u] >= 0) s += w[u] * v[u];
   }
   if constexpr (BF16)
     static_cast<bf4*>(a.y)[i] = __builtin_convertvector(s, bf4);
@@ -620,9 +674,12 @@ __global__ __launch_bounds__(256) void k_mxfp4_combine(Mxfp4CombineArgs a) {
 
 }  // namespace
 
-// Rows of a tile of the expert layer: 16 while experts hold a few rows each (straight from global memory), else
-// 128 (through LDS).
-int mxfp4_tile_rows(long long routes, int experts) { return routes <= 12LL * experts ? 16 : 128; }
+// Rows of a tile of the expert layer: 16 while experts hold a few rows each (straight from global memory; up to
+// kFewRoutesMax routes without a tile list), else 128 (through LDS).
+int mxfp4_tile_rows(long long routes, int experts) {
+  if (routes > 12LL * experts) return 128;
+  return routes <= kFewRoutesMax ? kFewRoutes : 16;
+}
 
 bool scales_aligned(const Mxfp4GemmArgs& a) {
   return a.K % 128 == 0 && a.K >= 512 &&
@@ -659,6 +716,13 @@ void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s) {
 
 template <int MODE>
 void launch_grouped(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) {
+  if (tile_rows == kFewRoutes) {
+    constexpr int FEW = MODE == kFc1 ? kFc1Few : kFc2Few;
+    const dim3 g((a.N + 63) / 64 * a.routes);
+    if (a.K <= 512) hipLaunchKernelGGL((k_mxfp4_rows<FEW, 1, 4, 4, 1, false>), g, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_mxfp4_rows<FEW, 1, 4, 4, 2, false>), g, dim3(256), 0, s, a);
+    return;
+  }
   if (tile_rows == 16) {
     const dim3 g((a.N + 63) / 64 * a.max_gtiles);
     if (a.K <= 512) hipLaunchKernelGGL((k_mxfp4_rows<MODE, 1, 4, 4, 1, false>), g, dim3(256), 0, s, a);

@@ -64,6 +64,8 @@ struct Mxfp4GemmArgs {
   const int32_t* num_gtiles;
   int max_gtiles;
   const int32_t* sorted;     // first product: slot -> route
+  const void* ids;           // few routes: [R] expert ids instead of a tile list (a slot is its route)
+  int ids64, routes, experts;
   int top_k;
   void* y;                   // dense: [T][N] fp32 or bf16; second product: fp32 [slots][N]
   uint8_t* bq;               // first product: [slots][N / 4] codes of silu(gate) * up (N = 2I)
@@ -72,7 +74,9 @@ struct Mxfp4GemmArgs {
 
 struct Mxfp4CombineArgs {
   const float* v;            // [slots][H]
-  const int32_t* route_slot; // [T][k], -1 = dropped
+  const int32_t* route_slot; // [T][k], -1 = dropped; null: a route's slot is the route itself, and
+  const void* ids;           //   ids outside [0, experts) are dropped
+  int ids64, experts;
   const float* w;            // [T][k]
   int tokens, top_k, H;
   void* y;                   // [T][H] fp32 or bf16
@@ -82,10 +86,12 @@ struct Mxfp4CombineArgs {
 void launch_mxfp4_quantize(const Mxfp4QuantArgs& a, int dtype, hipStream_t s);
 void launch_mxfp4_dequantize(const Mxfp4DequantArgs& a, int dtype, hipStream_t s);
 void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s);
-// tile_rows: rows of the tile list's tiles, as mxfp4_tile_rows chose them
+// tile_rows: rows of the tile list's tiles, as mxfp4_tile_rows chose them; kFewRoutes: no list
 void launch_mxfp4_fc1(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s);
 void launch_mxfp4_fc2(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s);
 void launch_mxfp4_combine(const Mxfp4CombineArgs& a, int y_dtype, hipStream_t s);
 int mxfp4_tile_rows(long long routes, int experts);
+constexpr int kFewRoutes = 1;
+constexpr int kFewRoutesMax = 256;               // one id a thread
 
 }  // namespace tmoe

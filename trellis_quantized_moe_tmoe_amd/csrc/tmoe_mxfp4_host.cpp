@@ -219,7 +219,11 @@ tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t p, const void* x, const void* i
   g.gtiles = m.gtiles;
   g.num_gtiles = m.num_gtiles;
   // every tile but an expert's last is full, and an expert without routes has none
-  g.max_gtiles = static_cast<int>(std::min<long long>(R, p->E + R / rows));
+  g.max_gtiles = rows == kFewRoutes ? 0 : static_cast<int>(std::min<long long>(R, p->E + R / rows));
+  g.ids = ids;
+  g.ids64 = p->ids64;
+  g.routes = static_cast<int>(R);
+  g.experts = p->E;
   g.sorted = m.sorted_routes;
   g.top_k = p->K;
   g.bq = at<uint8_t>(scratch, p->bq);
@@ -236,7 +240,10 @@ tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t p, const void* x, const void* i
 
   Mxfp4CombineArgs c;
   c.v = at<float>(scratch, p->v);
-  c.route_slot = m.route_slot;
+  c.route_slot = rows == kFewRoutes ? nullptr : m.route_slot;
+  c.ids = ids;
+  c.ids64 = p->ids64;
+  c.experts = p->E;
   c.w = w;
   c.tokens = T;
   c.top_k = p->K;
@@ -244,7 +251,7 @@ tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t p, const void* x, const void* i
   c.y = y;
 
   (void)hipGetLastError();
-  launch_route_map(m, nullptr, false, s);
+  if (rows != kFewRoutes) launch_route_map(m, nullptr, false, s);
   launch_mxfp4_quantize(q, TMOE_BF16, s);
   launch_mxfp4_fc1(g, rows, s);
   launch_mxfp4_fc2(h, rows, s);
