@@ -17,10 +17,33 @@ typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 
 enum { kDenseF32 = 0, kDenseBf16 = 1, kFc1 = 2, kFc2 = 3, kFc1Few = 4, kFc2Few = 5 };
 
-__device__ __forceinline__ f4 mma(i4v w, int ws, i4v x, int xs, f4 c) {
+// One 128-deep product; byte BYTE of the scale words holds this lane's scales.
+template <int BYTE>
+__device__ __forceinline__ f4 mma_byte(i4v w, int ws, i4v x, int xs, f4 c) {
   const i8v a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
   const i8v b = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, ws, 0, xs);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, BYTE, ws, BYTE, xs);
+}
+__device__ __forceinline__ f4 mma(int byte, i4v w, int ws, i4v x, int xs, f4 c) {   // byte: known once unrolled
+  return byte == 0 ? mma_byte<0>(w, ws, x, xs, c)
+       : byte == 1 ? mma_byte<1>(w, ws, x, xs, c)
+       : byte == 2 ? mma_byte<2>(w, ws, x, xs, c) : mma_byte<3>(w, ws, x, xs, c);
+}
+
+// N (1, 2 or 4) neighbouring scale bytes, first one in byte 0.
+template <int N>
+__device__ __forceinline__ int load_scale_bytes(const uint8_t* p) {
+  if constexpr (N == 1) {
+    return *p;
+  } else if constexpr (N == 2) {
+    uint16_t v;
+    __builtin_memcpy(&v, p, 2);
+    return v;
+  } else {
+    uint32_t v;
+    __builtin_memcpy(&v, p, 4);
+    return static_cast<int>(v);
+  }
 }
 
 // Four neighbouring columns col.. of a row of N, at element `at` of y; columns past N are dropped. QUADS: N
@@ -81,10 +104,12 @@ __device__ __forceinline__ void store_swiglu(const f4 (&g)[2], const f4 (&u)[2],
 }
 
 // Few rows: a workgroup of KW wavefronts computes 16 MT rows by 16 NT columns straight from global memory,
-// each wavefront every KW-th 128-deep step, their sums joined in LDS in a fixed order. What bounds it is the
-// latency of a wavefront's loads, so they are issued AH steps at a time (the weights first: they do not wait
+// each wavefront every KW-th batch of K, their sums joined in LDS in a fixed order. What bounds it is the
+// latency of a wavefront's loads, so they are issued AH 128-deep steps at a time (the weights first: they do not wait
 // for the tile's routes) and, with TWO, the next batch before the products of the one before; the expert
-// layer's products have many workgroups a CU instead, and few registers keep them there. Blocks past K repeat
+// layer's products have many workgroups a CU instead, and few registers keep them there. A batch is 4 AH
+// neighbouring blocks of every row; lane group q takes AH of them in a row, so that their scales are one
+// load (a byte load for each block took a third of the first product's time at T = 16). Blocks past K repeat
 // the last one with the scale 2^-127 on both sides (see the tiles below).
 //
 // kFc1Few, kFc2Few (up to kFewRoutesMax routes): there is no tile list. A workgroup stands for a route, finds
@@ -138,7 +163,7 @@ __global__ __launch_bounds__(64 * KW, TWO ? 2 : 5) void k_mxfp4_rows(Mxfp4GemmAr
     row0 = tile * 16 * MT;
     nrows = min(16 * MT, a.rows - row0);
   }
-  const int nblk = a.K / 32, steps = (nblk + 3) / 4;
+  const int nblk = a.K / 32, batches = (nblk + 4 * AH - 1) / (4 * AH);
   const uint8_t* wq = a.wq + expert * a.N * (a.K / 2);
   const uint8_t* ws = a.ws + expert * a.N * nblk;
 
@@ -153,32 +178,32 @@ __global__ __launch_bounds__(64 * KW, TWO ? 2 : 5) void k_mxfp4_rows(Mxfp4GemmAr
   }
   struct Batch {
     i4v w[AH][NT], x[AH][MT];
-    int ws[AH][NT], xs[AH][MT];
+    int ws[NT], xs[MT];
   };
-  auto load_w = [&](int st, Batch& b) {
+  auto scale_word = [&](const uint8_t* p, int blk) -> int {   // K / 32 >= AH; bytes past K are 0
+    const int from = min(blk, nblk - AH);
+    const uint32_t v = static_cast<uint32_t>(load_scale_bytes<AH>(p + from)) >> (8 * min(blk - from, AH - 1));
+    return blk < nblk ? static_cast<int>(v) : 0;
+  };
+  auto load_w = [&](int batch, Batch& b) {
+    const int blk = 4 * AH * batch + AH * q;
 #pragma unroll
-    for (int u = 0; u < AH; ++u) {
-      const int blk = 4 * (st + u * KW) + q, at = min(blk, nblk - 1);
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        b.w[u][n] = reinterpret_cast<const i4v*>(pq[n])[at];
-        b.ws[u][n] = ps[n][at];
-      }
+      for (int u = 0; u < AH; ++u) b.w[u][n] = reinterpret_cast<const i4v*>(pq[n])[min(blk + u, nblk - 1)];
+      b.ws[n] = scale_word(ps[n], blk);
     }
   };
-  auto load_x = [&](int st, Batch& b) {
+  auto load_x = [&](int batch, Batch& b) {
+    const int blk = 4 * AH * batch + AH * q;
 #pragma unroll
-    for (int u = 0; u < AH; ++u) {
-      const int blk = 4 * (st + u * KW) + q, at = min(blk, nblk - 1);
+    for (int m = 0; m < MT; ++m) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        b.x[u][m] = reinterpret_cast<const i4v*>(xq[m])[at];
-        b.xs[u][m] = xs[m][at];
-      }
+      for (int u = 0; u < AH; ++u) b.x[u][m] = reinterpret_cast<const i4v*>(xq[m])[min(blk + u, nblk - 1)];
+      b.xs[m] = scale_word(xs[m], blk);
     }
   };
   __shared__ f4 part[KW][MT * NT][64];
-  constexpr int kStride = KW * AH;
   Batch b0, b1;
   load_w(wv, b0);
   long long slot[MT];
@@ -197,41 +222,34 @@ __global__ __launch_bounds__(64 * KW, TWO ? 2 : 5) void k_mxfp4_rows(Mxfp4GemmAr
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = f4{0, 0, 0, 0};
-  auto multiply = [&](int st, const Batch& b) {
+  auto multiply = [&](const Batch& b) {
 #pragma unroll
-    for (int u = 0; u < AH; ++u) {
-      const bool in = 4 * (st + u * KW) + q < nblk;
-      int sx[MT], sw[NT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) sx[m] = in ? b.xs[u][m] : 0;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) sw[n] = in ? b.ws[u][n] : 0;
+    for (int u = 0; u < AH; ++u)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n] = mma(b.w[u][n], sw[n], b.x[u][m], sx[m], acc[m][n]);
-    }
+        for (int n = 0; n < NT; ++n) acc[m][n] = mma(u, b.w[u][n], b.ws[n], b.x[u][m], b.xs[m], acc[m][n]);
   };
-  int st = wv;
+  int at = wv;                                   // the batch in b0
   if constexpr (TWO) {
-    for (; st + kStride < steps; st += 2 * kStride) {
-      load_w(st + kStride, b1);
-      load_x(st + kStride, b1);
-      multiply(st, b0);
-      if (st + 2 * kStride < steps) {
-        load_w(st + 2 * kStride, b0);
-        load_x(st + 2 * kStride, b0);
+    for (; at + KW < batches; at += 2 * KW) {
+      load_w(at + KW, b1);
+      load_x(at + KW, b1);
+      multiply(b0);
+      if (at + 2 * KW < batches) {
+        load_w(at + 2 * KW, b0);
+        load_x(at + 2 * KW, b0);
       }
-      multiply(st + kStride, b1);
+      multiply(b1);
     }
-    if (st < steps) multiply(st, b0);
+    if (at < batches) multiply(b0);
   } else {
-    while (st < steps) {
-      multiply(st, b0);
-      st += kStride;
-      if (st < steps) {
-        load_w(st, b0);
-        load_x(st, b0);
+    while (at < batches) {
+      multiply(b0);
+      at += KW;
+      if (at < batches) {
+        load_w(at, b0);
+        load_x(at, b0);
       }
     }
   }
@@ -260,10 +278,10 @@ __global__ __launch_bounds__(64 * KW, TWO ? 2 : 5) void k_mxfp4_rows(Mxfp4GemmAr
       const f4 s = total(f);
       const int m = f / NT, n = f % NT;
       const int col = 16 * NT * group + 16 * n + 4 * q;
-      const long long at = (FEW ? slot[0] : row0 + 16 * m + r) * a.N + col;
+      const long long to = (FEW ? slot[0] : row0 + 16 * m + r) * a.N + col;
       if (16 * m + r >= nrows) continue;
-      if (a.N % 4 == 0) store4<MODE == kDenseBf16, true>(a.y, at, col, a.N, s);
-      else store4<MODE == kDenseBf16, false>(a.y, at, col, a.N, s);
+      if (a.N % 4 == 0) store4<MODE == kDenseBf16, true>(a.y, to, col, a.N, s);
+      else store4<MODE == kDenseBf16, false>(a.y, to, col, a.N, s);
     }
   }
 }
@@ -703,7 +721,8 @@ void launch_dense(const Mxfp4GemmArgs& a, hipStream_t s) {
   std::integral_constant<int, 1> one;
   std::integral_constant<int, 2> two;
   std::integral_constant<int, 4> four;
-  if (a.rows <= 16) rows(one, one, four);
+  if (a.K < 128) rows(four, two, one);           // the others read four or two neighbouring scales
+  else if (a.rows <= 16) rows(one, one, four);
   else if (a.rows <= 32) rows(two, one, two);
   else if (a.rows <= 64) rows(four, one, two);
   else rows(four, two, one);
