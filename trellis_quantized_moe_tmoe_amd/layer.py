@@ -47,13 +47,37 @@ def _same_device(named) -> None:
         raise ValueError(f"tensors must be on a GPU device, got {dev}")
 
 
-def _launch(device, fn, where: str, *args) -> None:
-    """fn(*args, stream) with `device` current and its current torch stream, raising on an error status."""
-    if device.index == torch.cuda.current_device():
-        check(fn(*args, _stream(device)), where)
+# The small calls of the router and of MXFP4 last a few microseconds on the GPU, so their wrappers keep the
+# host's share down: one comparison for a tensor that fits, the full check (and its message) only for one that
+# does not, and the current device and stream without building their Python objects.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _fits(t, shape, dtype) -> bool:
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _one_gpu(first, *others) -> bool:
+    index = first.get_device()
+    if not first.is_cuda:
+        return False
+    for t in others:
+        if t.get_device() != index:
+            return False
+    return True
+
+
+def _launch(index: int, fn, where: str, *args) -> None:
+    """fn(*args, stream) with GPU `index` current and its current torch stream, raising on an error status."""
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            check(fn(*args, _stream(device)), where)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        check(status, where)
 
 
 def _check_scratch(scratch, need: int) -> None:

@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from . import native
-from .layer import _BITS16, _check_scratch, _launch, _require, _same_device
+from .layer import _BITS16, _check_scratch, _fits, _launch, _one_gpu, _require, _same_device
 from .native import check, lib
 
 _DTYPES = {torch.float32: native.F32, torch.bfloat16: native.BF16, torch.float16: native.F16}
@@ -29,16 +29,18 @@ def quantize(x: torch.Tensor):
     """(codes uint8 [..., K/2], scales uint8 [..., K/32]) of fp32, bf16 or fp16 values [..., K], K a multiple of 32."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x: expected a tensor [..., K]")
-    K = x.shape[-1]
-    _require(x, "x", x.shape, tuple(_DTYPES))
+    lead, K = x.shape[:-1], x.shape[-1]
+    if x.dtype not in _DTYPES or not x.is_contiguous():
+        _require(x, "x", x.shape, tuple(_DTYPES))
     if K == 0 or K % 32:
         raise ValueError(f"x: the last dimension is {K}, expected a multiple of 32")
-    _same_device([("x", x)])
-    lead, rows = x.shape[:-1], x.numel() // K
-    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
-    _launch(x.device, lib.tmoe_mxfp4_quantize, "tmoe_mxfp4_quantize", x.data_ptr(), _DTYPES[x.dtype], rows, K,
-            codes.data_ptr(), scales.data_ptr())
+    if not x.is_cuda:
+        _same_device([("x", x)])
+    dev = x.device
+    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=dev)
+    _launch(dev.index, lib.tmoe_mxfp4_quantize, "tmoe_mxfp4_quantize", x.data_ptr(), _DTYPES[x.dtype], x.numel() // K,
+            K, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -46,11 +48,14 @@ def _operand(codes, scales, name: str, dim: Optional[int] = None) -> int:
     """K of an MXFP4 tensor, after checking its two parts against each other."""
     if not isinstance(codes, torch.Tensor) or codes.dim() < 1 or (dim is not None and codes.dim() != dim):
         raise ValueError(f"{name}: expected a tensor of codes" + (f" with {dim} dimensions" if dim else ""))
-    K = 2 * codes.shape[-1]
+    shape = codes.shape
+    K = 2 * shape[-1]
     if K == 0 or K % 32:
         raise ValueError(f"{name}: rows of {K} values, expected a multiple of 32")
-    _require(codes, f"{name} codes", codes.shape, (torch.uint8,))
-    _require(scales, f"{name} scales", (*codes.shape[:-1], K // 32), (torch.uint8,))
+    if not (codes.dtype is torch.uint8 and codes.is_contiguous()):
+        _require(codes, f"{name} codes", shape, (torch.uint8,))
+    if not _fits(scales, (*shape[:-1], K // 32), torch.uint8):
+        _require(scales, f"{name} scales", (*shape[:-1], K // 32), (torch.uint8,))
     return K
 
 
@@ -59,9 +64,11 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float32) -
     K = _operand(codes, scales, "x")
     if dtype not in _DTYPES:
         raise ValueError(f"dtype: {dtype}, expected one of {[str(d) for d in _DTYPES]}")
-    _same_device([("codes", codes), ("scales", scales)])
-    x = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
-    _launch(codes.device, lib.tmoe_mxfp4_dequantize, "tmoe_mxfp4_dequantize", codes.data_ptr(), scales.data_ptr(),
+    if not _one_gpu(codes, scales):
+        _same_device([("codes", codes), ("scales", scales)])
+    dev = codes.device
+    x = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=dev)
+    _launch(dev.index, lib.tmoe_mxfp4_dequantize, "tmoe_mxfp4_dequantize", codes.data_ptr(), scales.data_ptr(),
             x.numel() // K, K, _DTYPES[dtype], x.data_ptr())
     return x
 
@@ -72,13 +79,15 @@ def linear(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
     K = _operand(x_codes, x_scales, "x", 2)
     if _operand(w_codes, w_scales, "w", 2) != K:
         raise ValueError(f"w: rows of {2 * w_codes.shape[1]} values, x has {K}")
-    T, N, out = x_codes.shape[0], w_codes.shape[0], _out_dtype(out_dtype)
+    T, N, out, dev = x_codes.shape[0], w_codes.shape[0], _out_dtype(out_dtype), x_codes.device
     if y is None:
-        y = torch.empty((T, N), dtype=out_dtype, device=x_codes.device)
-    else:
+        y = torch.empty((T, N), dtype=out_dtype, device=dev)
+    elif not _fits(y, (T, N), out_dtype):
         _require(y, "y", (T, N), (out_dtype,))
-    _same_device([("x codes", x_codes), ("x scales", x_scales), ("w codes", w_codes), ("w scales", w_scales), ("y", y)])
-    _launch(y.device, lib.tmoe_linear_mxfp4, "tmoe_linear_mxfp4", x_codes.data_ptr(), x_scales.data_ptr(), T,
+    if not _one_gpu(x_codes, x_scales, w_codes, w_scales, y):
+        _same_device([("x codes", x_codes), ("x scales", x_scales), ("w codes", w_codes), ("w scales", w_scales),
+                      ("y", y)])
+    _launch(dev.index, lib.tmoe_linear_mxfp4, "tmoe_linear_mxfp4", x_codes.data_ptr(), x_scales.data_ptr(), T,
             w_codes.data_ptr(), w_scales.data_ptr(), K, N, out, y.data_ptr())
     return y
 
@@ -134,7 +143,7 @@ class ExpertPlan:
         if y is None and isinstance(x, torch.Tensor):
             y = torch.empty((max(T, 0), self.hidden), dtype=self.out_dtype, device=x.device)
         self.check_call(x, ids, w, weights, scratch, y)
-        _launch(x.device, lib.tmoe_forward_mxfp4, "tmoe_forward_mxfp4", self.handle, x.data_ptr(), ids.data_ptr(),
+        _launch(x.device.index, lib.tmoe_forward_mxfp4, "tmoe_forward_mxfp4", self.handle, x.data_ptr(), ids.data_ptr(),
                 w.data_ptr(), T, ctypes.byref(weights.c), y.data_ptr(), scratch.data_ptr(), scratch.numel())
         return y
 

@@ -10,74 +10,94 @@ capture."""
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
 
 from . import native
-from .layer import _launch, _require, _same_device
+from .layer import _fits, _launch, _one_gpu, _require, _same_device
 from .native import check, lib
 
 _DTYPES = {torch.float32: native.F32, torch.bfloat16: native.BF16, torch.float16: native.F16}
 _IDS = {torch.int32: native.IDS_I32, torch.int64: native.IDS_I64}
 
 
-def _config(logits, top_k: int, ids_dtype, renormalize: bool) -> native.RouterConfig:
+@functools.lru_cache(maxsize=256)
+def _packed(E: int, top_k: int, dtype, ids_dtype, renormalize: bool):
+    cfg = native.RouterConfig(E, top_k, _DTYPES[dtype], _IDS[ids_dtype], int(renormalize))
+    return ctypes.byref(cfg)                      # keeps cfg alive
+
+
+@functools.lru_cache(maxsize=256)
+def _scratch_bytes(cfg, T: int) -> int:
+    need = ctypes.c_size_t()
+    check(lib.tmoe_balance_loss_scratch(cfg, T, ctypes.byref(need)), "tmoe_balance_loss_scratch")
+    return need.value
+
+
+def _config(logits, top_k: int, ids_dtype, renormalize: bool):
+    """(configuration for the library, row stride) of logits that it can take."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits: expected a 2-D tensor [T, E]")
     if logits.dtype not in _DTYPES:
         raise ValueError(f"logits: dtype {logits.dtype}, expected one of {[str(d) for d in _DTYPES]}")
-    if logits.shape[0] > 0 and ((logits.shape[1] > 1 and logits.stride(1) != 1) or
-                                (logits.shape[0] > 1 and logits.stride(0) < logits.shape[1])):
+    (T, E), (row, step) = logits.shape, logits.stride()
+    if T > 0 and ((E > 1 and step != 1) or (T > 1 and row < E)):
         raise ValueError("logits: the values of a row must be adjacent and rows must not overlap")
     if ids_dtype not in _IDS:
         raise ValueError(f"ids: dtype {ids_dtype}, expected torch.int32 or torch.int64")
-    return native.RouterConfig(logits.shape[1], top_k, _DTYPES[logits.dtype], _IDS[ids_dtype], int(bool(renormalize)))
-
-
-def _row_stride(logits) -> int:
-    return logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+    return _packed(E, top_k, logits.dtype, ids_dtype, bool(renormalize)), row if T > 1 else E
 
 
 def _topk(logits, top_k, renormalize, token_mask, ids_dtype):
-    cfg = _config(logits, top_k, ids_dtype, renormalize)
-    T, dev = logits.shape[0], logits.device
-    named = [("logits", logits)]
+    cfg, stride = _config(logits, top_k, ids_dtype, renormalize)
+    T, dev, mask = logits.shape[0], logits.device, None
     if token_mask is not None:
         _require(token_mask, "token_mask", (T,), (torch.bool, torch.uint8))
-        named.append(("token_mask", token_mask))
-    _same_device(named)
+        if not _one_gpu(logits, token_mask):
+            _same_device([("logits", logits), ("token_mask", token_mask)])
+        mask = token_mask.data_ptr()
+    elif not logits.is_cuda:
+        _same_device([("logits", logits)])
     ids = torch.empty((T, top_k), dtype=ids_dtype, device=dev)
     w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     lse = torch.empty(T, dtype=torch.float32, device=dev)
-    _launch(dev, lib.tmoe_router_topk, "tmoe_router_topk", ctypes.byref(cfg), logits.data_ptr(), _row_stride(logits),
-            None if token_mask is None else token_mask.data_ptr(), T, ids.data_ptr(), w.data_ptr(), lse.data_ptr())
+    _launch(dev.index, lib.tmoe_router_topk, "tmoe_router_topk", cfg, logits.data_ptr(), stride, mask, T,
+            ids.data_ptr(), w.data_ptr(), lse.data_ptr())
     return ids, w, lse
 
 
 def _check_ids(ids, T: int) -> int:
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids: expected a 2-D tensor [T, k]")
-    _require(ids, "ids", (T, ids.shape[1]), tuple(_IDS))
-    return ids.shape[1]
+    k = ids.shape[1]
+    if not (ids.dtype in _IDS and ids.shape[0] == T and ids.is_contiguous()):
+        _require(ids, "ids", (T, k), tuple(_IDS))
+    return k
+
+
+def _tokens(logits) -> int:
+    return logits.shape[0] if isinstance(logits, torch.Tensor) and logits.dim() == 2 else 0
 
 
 def _balance_loss(logits, lse, ids, coefficient):
-    T = logits.shape[0] if isinstance(logits, torch.Tensor) and logits.dim() == 2 else 0
+    T = _tokens(logits)
     k = _check_ids(ids, T)
-    cfg = _config(logits, k, ids.dtype, True)
-    _require(lse, "lse", (T,), (torch.float32,))
-    _same_device([("logits", logits), ("lse", lse), ("ids", ids)])
+    cfg, stride = _config(logits, k, ids.dtype, True)
+    if not _fits(lse, (T,), torch.float32):
+        _require(lse, "lse", (T,), (torch.float32,))
+    if not _one_gpu(logits, lse, ids):
+        _same_device([("logits", logits), ("lse", lse), ("ids", ids)])
     E, dev = logits.shape[1], logits.device
-    need = ctypes.c_size_t()
-    check(lib.tmoe_balance_loss_scratch(ctypes.byref(cfg), T, ctypes.byref(need)), "tmoe_balance_loss_scratch")
-    scratch = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    need = _scratch_bytes(cfg, T)
+    scratch = torch.empty(need, dtype=torch.uint8, device=dev)
     loss = torch.empty((), dtype=torch.float32, device=dev)
     counts = torch.empty(E, dtype=torch.int32, device=dev)
     slope = torch.empty(E, dtype=torch.float32, device=dev)
-    _launch(dev, lib.tmoe_balance_loss, "tmoe_balance_loss", ctypes.byref(cfg), logits.data_ptr(), _row_stride(logits),
-            lse.data_ptr(), ids.data_ptr(), T, float(coefficient), loss.data_ptr(), counts.data_ptr(),
-            slope.data_ptr(), scratch.data_ptr(), need.value)
+    _launch(dev.index, lib.tmoe_balance_loss, "tmoe_balance_loss", cfg, logits.data_ptr(), stride, lse.data_ptr(),
+            ids.data_ptr(), T, float(coefficient), loss.data_ptr(), counts.data_ptr(), slope.data_ptr(),
+            scratch.data_ptr(), need)
     return loss, counts, slope
 
 
@@ -86,31 +106,36 @@ def backward(logits: torch.Tensor, lse: torch.Tensor, ids: torch.Tensor, *, w: O
              dloss: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of the logits [T, E], in their type, from the weights' gradient (w and dw [T, k]) and/or the
     balance loss's (slope [E] as `balance_loss` returns it, and dloss, one value on the GPU)."""
-    T = logits.shape[0] if isinstance(logits, torch.Tensor) and logits.dim() == 2 else 0
+    T = _tokens(logits)
     k = _check_ids(ids, T)
-    cfg = _config(logits, k, ids.dtype, renormalize)
+    cfg, stride = _config(logits, k, ids.dtype, renormalize)
     E, dev = logits.shape[1], logits.device
     if (w is None) != (dw is None) or (slope is None) != (dloss is None) or (w is None and slope is None):
         raise ValueError("give w and dw, slope and dloss, or all four")
-    _require(lse, "lse", (T,), (torch.float32,))
-    named = [("logits", logits), ("lse", lse), ("ids", ids)]
+    if not _fits(lse, (T,), torch.float32):
+        _require(lse, "lse", (T,), (torch.float32,))
+    tensors, pw, pdw, pslope, pdloss = [lse, ids], None, None, None, None
     if w is not None:
-        _require(w, "w", (T, k), (torch.float32,))
-        _require(dw, "dw", (T, k), (torch.float32,))
-        named += [("w", w), ("dw", dw)]
+        for name, t in (("w", w), ("dw", dw)):
+            if not _fits(t, (T, k), torch.float32):
+                _require(t, name, (T, k), (torch.float32,))
+        tensors += [w, dw]
+        pw, pdw = w.data_ptr(), dw.data_ptr()
     if slope is not None:
-        _require(slope, "slope", (E,), (torch.float32,))
+        if not _fits(slope, (E,), torch.float32):
+            _require(slope, "slope", (E,), (torch.float32,))
         if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1 or dloss.dtype != torch.float32:
             raise ValueError("dloss: expected one fp32 value in a tensor")
-        named += [("slope", slope), ("dloss", dloss)]
-    _same_device(named)
+        tensors += [slope, dloss]
+        pslope, pdloss = slope.data_ptr(), dloss.data_ptr()
+    if not _one_gpu(logits, *tensors):
+        _same_device([("logits", logits), ("lse", lse), ("ids", ids)] + [
+            (n, t) for n, t in (("w", w), ("dw", dw), ("slope", slope), ("dloss", dloss)) if t is not None])
     d = torch.empty((T, E), dtype=logits.dtype, device=dev)
     if T == 0:                                    # empty tensors have no address to tell the parts by
         return d
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _launch(dev, lib.tmoe_router_backward, "tmoe_router_backward", ctypes.byref(cfg), logits.data_ptr(),
-            _row_stride(logits), lse.data_ptr(), ids.data_ptr(), ptr(w), ptr(dw), ptr(slope), ptr(dloss), T,
-            d.data_ptr())
+    _launch(dev.index, lib.tmoe_router_backward, "tmoe_router_backward", cfg, logits.data_ptr(), stride,
+            lse.data_ptr(), ids.data_ptr(), pw, pdw, pslope, pdloss, T, d.data_ptr())
     return d
 
 
