@@ -387,9 +387,11 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     else col = min(cg * S::TC + j, a.N - 1);
     return scales ? ws + col * nblk : wq + col * (a.K / 2);
   };
+  // copies in the order weights, tokens: a token's address may wait for its route
   const uint8_t* src[S::LPP];
+  auto place_of = [&](int i) { return wv + 4 * (i < S::TC / 32 ? S::TR / 32 + i : i - S::TC / 32); };
 #pragma unroll
-  for (int i = 0; i < S::LPP; ++i) src[i] = source(8 * (wv + 4 * i) + (lane >> 3), false);
+  for (int i = 0; i < S::LPP; ++i) src[i] = source(8 * place_of(i) + (lane >> 3), false);
   const uint8_t* ssrc[S::SPT];
 #pragma unroll
   for (int i = 0; i < S::SPT; ++i) {
@@ -402,7 +404,7 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     const int blk = min(8 * pair + chunk, nblk - 1);
     __builtin_amdgcn_global_load_lds(
         (const void __attribute__((address_space(1)))*)(src[i] + 16 * blk),
-        (void __attribute__((address_space(3)))*)(lds + (pair & 1) * S::kSlot + (wv + 4 * i) * 1024), 16, 0, 0);
+        (void __attribute__((address_space(3)))*)(lds + (pair & 1) * S::kSlot + place_of(i) * 1024), 16, 0, 0);
   };
   // Scales of steps 4 g .. 4 g + 3: bytes 16 g .. of each row. The last group's load starts where it ends with
   // the row and is shifted when it is stored; rows shorter than 16 bytes have one
@@ -644,8 +646,8 @@ __global__ __launch_bounds__(256, 2) void k_mxfp4_tile_grouped(Mxfp4GemmArgs a, 
   __shared__ __align__(16) uint8_t lds[S::kLds];
   const int i = blockIdx.x / 8;
   const int tile = i / col_tiles * 8 + blockIdx.x % 8, ct = i % col_tiles;
+  const int4 t = a.gtiles[min(tile, a.max_gtiles - 1)];      // read beside the count, not after it
   if (tile >= *a.num_gtiles) return;
-  const int4 t = a.gtiles[tile];
   const long long expert = t.x & 0xffffff;
   if (t.z > 64) tile_body<MODE, 2, 2, 2, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
   else tile_body<MODE, 2, 2, 1, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);

@@ -12,56 +12,12 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  uint32_t o = __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);   // quad_perm 1,0,3,2
-  v = o > v ? o : v;
-  o = __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);            // quad_perm 2,3,0,1
-  return o > v ? o : v;
-}
-
-template <int DT>
-__device__ __forceinline__ void load8(const void* x, long long g, float (&v)[8]) {
-  if constexpr (DT == TMOE_F32) {
-    const float4* p = static_cast<const float4*>(x) + 2 * g;
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 q = static_cast<const uint4*>(x)[g];
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == TMOE_BF16) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      } else {
-        v[2 * i] = h2f(static_cast<uint16_t>(u[i] & 0xffffu));
-        v[2 * i + 1] = h2f(static_cast<uint16_t>(u[i] >> 16));
-      }
-    }
-  }
-}
-
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_mxfp4_quantize(Mxfp4QuantArgs a) {
   // whole quads are in range together: the group count is a multiple of four
   for (long long g = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; g < a.groups;
-       g += static_cast<long long>(gridDim.x) * kThreads) {
-    float v[8];
-    load8<DT>(a.x, g, v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-      m = b > m ? b : m;
-    }
-    const uint32_t byte = mxfp4_scale_byte(quad_max(m));
-    const float inv = mxfp4_inverse_scale(byte);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= inv;
-    reinterpret_cast<uint32_t*>(a.codes)[g] = byte == 255u ? 0u : mxfp4_codes8(v);
-    if ((threadIdx.x & 3) == 0) a.scales[g >> 2] = static_cast<uint8_t>(byte);
-  }
+       g += static_cast<long long>(gridDim.x) * kThreads)
+    mxfp4_quantize_group<DT>(a, g);
 }
 
 __device__ __forceinline__ uint16_t bf16_rne(float f) {

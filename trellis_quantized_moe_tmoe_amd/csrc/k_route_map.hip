@@ -16,6 +16,7 @@
 #include "tmoe_internal.hpp"
 #include "tmoe_rowbody.hpp"
 #include "tmoe_routemap.hpp"
+#include "tmoe_mxfp4.hpp"
 
 namespace tmoe {
 
@@ -23,6 +24,15 @@ namespace {
 
 constexpr int kWaves = 16;           // 1024 threads
 constexpr int kMaxExperts = 512;
+
+// What the workgroups past the route map's own do: nothing, the input rotation, or the MXFP4 quantisation of
+// a bf16 input (1024 groups of eight values each).
+enum { kPreNone = 0, kPreRotate = 1, kPreMxfp4 = 2 };
+
+__device__ __forceinline__ void quantize_groups(const Mxfp4QuantArgs& q, long long wg) {
+  const long long g = wg * 1024 + threadIdx.x;
+  if (g < q.groups) mxfp4_quantize_group<TMOE_BF16>(q, g);   // groups come in whole quads
+}
 
 // Exclusive scans of four values per thread over the workgroup at once; totals returned in *total.
 __device__ int4 block_exclusive_scan4(int4 v, int4* smem, int4* total) {
@@ -188,12 +198,18 @@ __device__ int publish_tables(const RouteMapArgs& a, int total_e, int bad, int4*
 }
 
 // All routes in one workgroup (workgroup 0): each wave takes a contiguous segment of R/16 routes.
-// Workgroups 1.. rotate the input rows, 16 items each (ROT = false: none).
-template <bool ROT, int EPL, bool MX>
-__global__ __launch_bounds__(1024) void k_route_map(RouteMapArgs a, RotateArgs ra) {
-  if constexpr (ROT) {
+// Workgroups 1.. rotate the input rows, 16 items each, or quantise them (PRE).
+template <int PRE, int EPL, bool MX>
+__global__ __launch_bounds__(1024) void k_route_map(RouteMapArgs a, RotateArgs ra, Mxfp4QuantArgs qa) {
+  if constexpr (PRE == kPreRotate) {
     if (blockIdx.x > 0) {
       rotate_routes<EPL, MX>(ra, (blockIdx.x - 1) * kWaves);
+      return;
+    }
+  }
+  if constexpr (PRE == kPreMxfp4) {
+    if (blockIdx.x > 0) {
+      quantize_groups(qa, blockIdx.x - 1);
       return;
     }
   }
@@ -236,11 +252,17 @@ __global__ __launch_bounds__(1024) void k_route_map(RouteMapArgs a, RotateArgs r
 // per expert into wg_counts[g][0..E) and its invalid ids into wg_counts[g][E]. Workgroups past the
 // counting ones rotate the input rows, 16 items each (the first third of the rotation groups; the
 // placement launch takes the rest).
-template <bool ROT, int EPL, bool MX>
-__global__ __launch_bounds__(1024) void k_route_count(RouteMapArgs a, RotateArgs ra, int count_groups) {
-  if constexpr (ROT) {
+template <int PRE, int EPL, bool MX>
+__global__ __launch_bounds__(1024) void k_route_count(RouteMapArgs a, RotateArgs ra, Mxfp4QuantArgs qa, int count_groups) {
+  if constexpr (PRE == kPreRotate) {
     if (static_cast<int>(blockIdx.x) >= count_groups) {
       rotate_routes<EPL, MX>(ra, (blockIdx.x - count_groups) * kWaves);
+      return;
+    }
+  }
+  if constexpr (PRE == kPreMxfp4) {
+    if (static_cast<int>(blockIdx.x) >= count_groups) {
+      quantize_groups(qa, blockIdx.x - count_groups);
       return;
     }
   }
@@ -275,9 +297,9 @@ __global__ __launch_bounds__(1024) void k_route_count(RouteMapArgs a, RotateArgs
 // earlier waves of this workgroup + earlier lanes of its chunk: stable token-major order.
 // Workgroups past the placing ones rotate the input rows from rotation group rot_first on (the
 // rotation is split between the two launches, so each overlaps its own share).
-template <bool ROT, int EPL, bool MX>
+template <int PRE, int EPL, bool MX>
 __global__ __launch_bounds__(1024) void k_route_place(RouteMapArgs a, RotateArgs ra, int place_groups, int rot_first) {
-  if constexpr (ROT) {
+  if constexpr (PRE == kPreRotate) {
     if (static_cast<int>(blockIdx.x) >= place_groups) {
       rotate_routes<EPL, MX>(ra, (static_cast<int>(blockIdx.x) - place_groups + rot_first) * kWaves);
       return;
@@ -354,19 +376,20 @@ void launch_route_map(const RouteMapArgs& a, const RotateArgs* ra, bool mx, hipS
   const RotateArgs none{};
   const RotateArgs& r = ra ? *ra : none;
   auto go = [&](auto rot, auto epl, auto m) {
-    constexpr bool ROT = decltype(rot)::value;
+    constexpr int PRE = decltype(rot)::value ? kPreRotate : kPreNone;
     constexpr int E = decltype(epl)::value;
     constexpr bool M = decltype(m)::value;
     if (a.routes <= kRouteSingleMax) {
-      hipLaunchKernelGGL((k_route_map<ROT, E, M>), dim3(1 + rot_groups), dim3(1024), 0, s, a, r);
+      hipLaunchKernelGGL((k_route_map<PRE, E, M>), dim3(1 + rot_groups), dim3(1024), 0, s, a, r, Mxfp4QuantArgs{});
       return;
     }
     const int groups = (a.routes + kRouteChunk - 1) / kRouteChunk;
     // a third of the rotation with the counting, two thirds with the placement (measured best of
     // 1/3, 1/2, 2/3: prefill route stage 23.0 -> 19.5 us against all of it in the first launch)
     const unsigned rot_count = rot_groups / 3, rot_place = rot_groups - rot_count;
-    hipLaunchKernelGGL((k_route_count<ROT, E, M>), dim3(groups + rot_count), dim3(1024), 0, s, a, r, groups);
-    hipLaunchKernelGGL((k_route_place<ROT, E, M>), dim3(groups + rot_place), dim3(1024), 0, s, a, r, groups,
+    hipLaunchKernelGGL((k_route_count<PRE, E, M>), dim3(groups + rot_count), dim3(1024), 0, s, a, r, Mxfp4QuantArgs{},
+                       groups);
+    hipLaunchKernelGGL((k_route_place<PRE, E, M>), dim3(groups + rot_place), dim3(1024), 0, s, a, r, groups,
                        static_cast<int>(rot_count));
   };
   if (!ra) {
@@ -377,6 +400,18 @@ void launch_route_map(const RouteMapArgs& a, const RotateArgs* ra, bool mx, hipS
     if (mx) go(std::true_type{}, epl, std::true_type{});
     else go(std::true_type{}, epl, std::false_type{});
   });
+}
+
+void launch_route_map_mxfp4(const RouteMapArgs& a, const Mxfp4QuantArgs& q, hipStream_t s) {
+  const unsigned extra = static_cast<unsigned>((q.groups + 1023) / 1024);
+  const RotateArgs none{};
+  if (a.routes <= kRouteSingleMax) {
+    hipLaunchKernelGGL((k_route_map<kPreMxfp4, 1, false>), dim3(1 + extra), dim3(1024), 0, s, a, none, q);
+    return;
+  }
+  const int groups = (a.routes + kRouteChunk - 1) / kRouteChunk;
+  hipLaunchKernelGGL((k_route_count<kPreMxfp4, 1, false>), dim3(groups + extra), dim3(1024), 0, s, a, none, q, groups);
+  hipLaunchKernelGGL((k_route_place<kPreNone, 1, false>), dim3(groups), dim3(1024), 0, s, a, none, groups, 0);
 }
 
 }  // namespace tmoe

@@ -4,9 +4,12 @@
 // elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one E8M0 scale byte (2^(byte - 127),
 // 255 = NaN) per block. Element 2i of a row is the low nibble of byte i.
 #pragma once
+#include "tmoe.h"
 #include "tmoe_device.hpp"
 
 namespace tmoe {
+
+struct RouteMapArgs;
 
 // Scale byte of a block with the largest magnitude amax, given as the bits of |amax|: the smallest
 // power of two 2^e with amax / 2^e <= 6 (so nothing saturates), e >= -127. amax = 2^x * 1.m lies in
@@ -42,6 +45,56 @@ struct Mxfp4QuantArgs {
   uint8_t* codes;            // [rows][cols / 2]
   uint8_t* scales;           // [rows][cols / 32]
 };
+
+// Quantises eight neighbouring values (group g); the four lanes of a block exchange their largest magnitude (as
+// integer bits, so infinities and NaNs win) by quad permutes: whole quads call it together.
+__device__ __forceinline__ uint32_t mxfp4_quad_max(uint32_t v) {
+  uint32_t o = __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);   // quad_perm 1,0,3,2
+  v = o > v ? o : v;
+  o = __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);            // quad_perm 2,3,0,1
+  return o > v ? o : v;
+}
+
+template <int DT>
+__device__ __forceinline__ void mxfp4_load8(const void* x, long long g, float (&v)[8]) {
+  if constexpr (DT == TMOE_F32) {
+    const float4* p = static_cast<const float4*>(x) + 2 * g;
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 q = static_cast<const uint4*>(x)[g];
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == TMOE_BF16) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      } else {
+        v[2 * i] = h2f(static_cast<uint16_t>(u[i] & 0xffffu));
+        v[2 * i + 1] = h2f(static_cast<uint16_t>(u[i] >> 16));
+      }
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void mxfp4_quantize_group(const Mxfp4QuantArgs& a, long long g) {
+  float v[8];
+  mxfp4_load8<DT>(a.x, g, v);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+    m = b > m ? b : m;
+  }
+  const uint32_t byte = mxfp4_scale_byte(mxfp4_quad_max(m));
+  const float inv = mxfp4_inverse_scale(byte);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= inv;
+  reinterpret_cast<uint32_t*>(a.codes)[g] = byte == 255u ? 0u : mxfp4_codes8(v);
+  if ((threadIdx.x & 3) == 0) a.scales[g >> 2] = static_cast<uint8_t>(byte);
+}
 
 struct Mxfp4DequantArgs {
   const uint8_t* codes;
@@ -84,6 +137,8 @@ struct Mxfp4CombineArgs {
 
 // dtype: TMOE_F32, TMOE_BF16 or TMOE_F16
 void launch_mxfp4_quantize(const Mxfp4QuantArgs& a, int dtype, hipStream_t s);
+// the route map and, in the same launch (extra workgroups, independent work), the bf16 input's quantisation
+void launch_route_map_mxfp4(const RouteMapArgs& a, const Mxfp4QuantArgs& q, hipStream_t s);
 void launch_mxfp4_dequantize(const Mxfp4DequantArgs& a, int dtype, hipStream_t s);
 void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s);
 // tile_rows: rows of the tile list's tiles, as mxfp4_tile_rows chose them; kFewRoutes: no list

@@ -251,8 +251,8 @@ tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t p, const void* x, const void* i
   c.y = y;
 
   (void)hipGetLastError();
-  if (rows != kFewRoutes) launch_route_map(m, nullptr, false, s);
-  launch_mxfp4_quantize(q, TMOE_BF16, s);
+  if (rows == kFewRoutes) launch_mxfp4_quantize(q, TMOE_BF16, s);
+  else launch_route_map_mxfp4(m, q, s);
   launch_mxfp4_fc1(g, rows, s);
   launch_mxfp4_fc2(h, rows, s);
   launch_mxfp4_combine(c, p->y_dtype, s);
