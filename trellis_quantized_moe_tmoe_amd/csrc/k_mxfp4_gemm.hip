@@ -71,6 +71,12 @@ __device__ __forceinline__ void store4(void* y, long long at, int col, int N, f4
   }
 }
 
+// x / (1 + exp(-x)) with the hardware's 2^y and reciprocal (one unit in the last place each, and |x| half steps
+// from the exponent's product): a few 2^-24 beside the 2^-4 of the codes that follow.
+__device__ __forceinline__ float silu(float x) {
+  return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+}
+
 // silu(g) * u, then the MXFP4 block of 32 neighbouring columns: a lane holds four of them in each of two
 // fragments, the lanes 16 apart the others.
 __device__ __forceinline__ void store_swiglu(const f4 (&g)[2], const f4 (&u)[2], uint8_t* bq, uint8_t* bs, int lane,
@@ -81,8 +87,7 @@ __device__ __forceinline__ void store_swiglu(const f4 (&g)[2], const f4 (&u)[2],
   for (int f = 0; f < 2; ++f)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float x = g[f][i];
-      h[4 * f + i] = x / (1.0f + expf(-x)) * u[f][i];
+      h[4 * f + i] = silu(g[f][i]) * u[f][i];
       const uint32_t b = __float_as_uint(h[4 * f + i]) & 0x7fffffffu;
       m = b > m ? b : m;
     }
@@ -331,8 +336,7 @@ __device__ __forceinline__ void store_swiglu32(const f16v& g, const f16v& u, uin
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float x = g[i];
-    v[i] = x / (1.0f + expf(-x)) * u[i];
+    v[i] = silu(g[i]) * u[i];
     const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
     m = b > m ? b : m;
   }
@@ -623,7 +627,7 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
 // Dense: row tiles by column tiles in groups of eight row tiles, a contiguous run of them to each of the
 // eight XCDs (workgroups are dealt to the XCDs in turn), so that an XCD's L2 holds what its tiles share.
 template <int MODE, int WT, int WC, int MT, int NT, bool ALIGNED>
-__global__ __launch_bounds__(256, 1) void k_mxfp4_tile_dense(Mxfp4GemmArgs a, int row_tiles, int col_tiles) {
+__global__ __launch_bounds__(256, MT * NT > 8 ? 1 : 2) void k_mxfp4_tile_dense(Mxfp4GemmArgs a, int row_tiles, int col_tiles) {
   using S = Tile<MODE, WT, WC, MT, NT>;
   __shared__ __align__(16) uint8_t lds[S::kLds];
   const int total = row_tiles * col_tiles, per = gridDim.x / 8;
@@ -706,28 +710,41 @@ bool scales_aligned(const Mxfp4GemmArgs& a) {
          ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
 }
 
+template <int MODE, int MT, int NT>
+void launch_tiles(const Mxfp4GemmArgs& a, hipStream_t s) {
+  using S = Tile<MODE, 2, 2, MT, NT>;
+  const int rt = (a.rows + S::TR - 1) / S::TR, ct = (a.N + S::TC - 1) / S::TC;
+  const dim3 g((rt * ct + 7) / 8 * 8);
+  if (scales_aligned(a)) hipLaunchKernelGGL((k_mxfp4_tile_dense<MODE, 2, 2, MT, NT, true>), g, dim3(256), 0, s, a, rt, ct);
+  else hipLaunchKernelGGL((k_mxfp4_tile_dense<MODE, 2, 2, MT, NT, false>), g, dim3(256), 0, s, a, rt, ct);
+}
+
+template <int MODE, int MT, int NT, int AH>
+void launch_rows(const Mxfp4GemmArgs& a, hipStream_t s) {
+  const int groups = (a.N + 16 * NT - 1) / (16 * NT), tiles = (a.rows + 16 * MT - 1) / (16 * MT);
+  hipLaunchKernelGGL((k_mxfp4_rows<MODE, MT, NT, 8, AH, true>), dim3(groups * tiles), dim3(512), 0, s, a);
+}
+
+// The shape of the dense product, by the number of 128 x 128 tiles (us; K = 4096 unless said):
+//   T <= 64         wavefronts that split K (T = 48, N = 1024: 7.6, 64 x 128 tiles 8.5; K = 2560: 5.1 and 6.4)
+//   up to 160 tiles 64 x 128, two workgroups a CU (T = 400, N = 4096: 9.5; 128 x 128 11.6, 256 x 256 26.5)
+//   up to 512 tiles 128 x 128, two workgroups a CU (T = 1600, N = 4096: 23.4; 64 x 128 33.5, 256 x 256 30.6)
+//   more            256 x 256, one workgroup a CU: half the LDS traffic for each product (T = 3200, N = 4096:
+//                   36.8; 128 x 128 46.4)
 template <int MODE>
 void launch_dense(const Mxfp4GemmArgs& a, hipStream_t s) {
-  const int rt = (a.rows + 255) / 256, ct = (a.N + 255) / 256;
-  if (rt * ct >= 64) {
-    const dim3 g((rt * ct + 7) / 8 * 8);
-    if (scales_aligned(a)) hipLaunchKernelGGL((k_mxfp4_tile_dense<MODE, 2, 2, 4, 4, true>), g, dim3(256), 0, s, a, rt, ct);
-    else hipLaunchKernelGGL((k_mxfp4_tile_dense<MODE, 2, 2, 4, 4, false>), g, dim3(256), 0, s, a, rt, ct);
-    return;
+  const long long tiles = ((a.rows + 127LL) / 128) * ((a.N + 127) / 128);
+  if (a.rows <= 64 && a.K >= 128) {              // they read four or two neighbouring scales
+    if (a.rows <= 16) launch_rows<MODE, 1, 1, 4>(a, s);
+    else if (a.rows <= 32) launch_rows<MODE, 2, 1, 2>(a, s);
+    else launch_rows<MODE, 4, 1, 2>(a, s);
+  } else if (tiles <= 160) {
+    launch_tiles<MODE, 1, 2>(a, s);
+  } else if (tiles <= 512) {
+    launch_tiles<MODE, 2, 2>(a, s);
+  } else {
+    launch_tiles<MODE, 4, 4>(a, s);
   }
-  auto rows = [&](auto mt, auto nt, auto ah) {
-    constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, AH = decltype(ah)::value;
-    const int groups = (a.N + 16 * NT - 1) / (16 * NT), tiles = (a.rows + 16 * MT - 1) / (16 * MT);
-    hipLaunchKernelGGL((k_mxfp4_rows<MODE, MT, NT, 8, AH, true>), dim3(groups * tiles), dim3(512), 0, s, a);
-  };
-  std::integral_constant<int, 1> one;
-  std::integral_constant<int, 2> two;
-  std::integral_constant<int, 4> four;
-  if (a.K < 128) rows(four, two, one);           // the others read four or two neighbouring scales
-  else if (a.rows <= 16) rows(one, one, four);
-  else if (a.rows <= 32) rows(two, one, two);
-  else if (a.rows <= 64) rows(four, one, two);
-  else rows(four, two, one);
 }
 
 void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s) {
