@@ -412,7 +412,7 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
   };
   // Scales of steps 4 g .. 4 g + 3: bytes 16 g .. of each row. The last group's load starts where it ends with
   // the row and is shifted when it is stored; rows shorter than 16 bytes have one
-  // group, read byte by byte before the loop (the loop's fetches then read 16 bytes of codes for nothing).
+  // group, read before the loop (the loop's fetches then read 16 bytes of codes for nothing).
   auto copy_scales = [&](int g) {                // ALIGNED: 64 rows of 16 bytes a copy, repeats at the end
     const int from = min(16 * g, nblk - 16);
 #pragma unroll
@@ -456,10 +456,38 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
       store_scales(0);
       return;
     }
+    // rows of less than 16 bytes: 16 bytes that lie in the array, shifted to the row's first and cut behind its last
+    const long long tokens = MODE == kFc1 ? a.routes / a.top_k : MODE == kFc2 ? a.routes : a.rows;
+    const uint8_t* x_end = a.xs + tokens * nblk;
+    const uint8_t* w_end = ws + static_cast<long long>(a.N) * nblk;    // the expert's own rows
     uint8_t* buf = lds + 2 * S::kSlot;
-    for (int i = tid; i < S::TR + S::TC; i += 256) {
-      const uint8_t* p = source(i, true);
-      for (int b = 0; b < 16; ++b) buf[16 * i + b] = b < nblk ? p[b] : 0;
+#pragma unroll
+    for (int i = 0; i < S::SPT; ++i) {
+      const int at = min(tid + 256 * i, S::TR + S::TC - 1);
+      const uint8_t* p = source(at, true);
+      const uint8_t* end = at < S::TR ? x_end : w_end;
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (end - (at < S::TR ? a.xs : ws) >= 16) {
+        const uint8_t* from = p + 16 <= end ? p : end - 16;
+        const int by = static_cast<int>(p - from);
+        __builtin_memcpy(w, from, 16);
+#pragma unroll
+        for (int d = 2; d; d >>= 1)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w[q] = by & (4 * d) ? (q + d < 4 ? w[q + d] : 0u) : w[q];
+        const uint32_t b = by & 3;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = __builtin_amdgcn_alignbyte(q < 3 ? w[q + 1] : 0u, w[q], b);
+      } else {
+#pragma unroll
+        for (int b = 0; b < 15; ++b) w[b >> 2] |= static_cast<uint32_t>(p[min(b, nblk - 1)]) << (8 * (b & 3));
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int have = max(0, min(4, nblk - 4 * q));
+        w[q] = have == 4 ? w[q] : w[q] & ((1u << (8 * have)) - 1u);
+      }
+      reinterpret_cast<uint4*>(buf)[at] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   };
 
@@ -701,7 +729,7 @@ __global__ __launch_bounds__(256) void k_mxfp4_combine(Mxfp4CombineArgs a) {
 // Rows of a tile of the expert layer: 16 while experts hold a few rows each (straight from global memory; up to
 // kFewRoutesMax routes without a tile list), else 128 (through LDS).
 int mxfp4_tile_rows(long long routes, int experts) {
-  if (routes > 12LL * experts) return 128;
+  if (routes > 10LL * experts) return 128;
   return routes <= kFewRoutesMax ? kFewRoutes : 16;
 }
 
@@ -752,21 +780,20 @@ void launch_mxfp4_dense(const Mxfp4GemmArgs& a, int y_dtype, hipStream_t s) {
   else launch_dense<kDenseF32>(a, s);
 }
 
+// Few rows an expert: one 128-deep step a wavefront and batch up to K = 512, two up to K = 1024 (one batch), two and
+// the next batch ahead beyond (H = 2560, T = 16: 25.6 -> 22.5 us; one batch: 13.5 -> 15.3 with it).
+template <int MODE>
+void launch_few_rows(const Mxfp4GemmArgs& a, int tiles, hipStream_t s) {
+  const dim3 g((a.N + 63) / 64 * tiles), b(256);
+  if (a.K <= 512) hipLaunchKernelGGL((k_mxfp4_rows<MODE, 1, 4, 4, 1, false>), g, b, 0, s, a);
+  else if (a.K <= 1024) hipLaunchKernelGGL((k_mxfp4_rows<MODE, 1, 4, 4, 2, false>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((k_mxfp4_rows<MODE, 1, 4, 4, 2, true>), g, b, 0, s, a);
+}
+
 template <int MODE>
 void launch_grouped(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) {
-  if (tile_rows == kFewRoutes) {
-    constexpr int FEW = MODE == kFc1 ? kFc1Few : kFc2Few;
-    const dim3 g((a.N + 63) / 64 * a.routes);
-    if (a.K <= 512) hipLaunchKernelGGL((k_mxfp4_rows<FEW, 1, 4, 4, 1, false>), g, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_mxfp4_rows<FEW, 1, 4, 4, 2, false>), g, dim3(256), 0, s, a);
-    return;
-  }
-  if (tile_rows == 16) {
-    const dim3 g((a.N + 63) / 64 * a.max_gtiles);
-    if (a.K <= 512) hipLaunchKernelGGL((k_mxfp4_rows<MODE, 1, 4, 4, 1, false>), g, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_mxfp4_rows<MODE, 1, 4, 4, 2, false>), g, dim3(256), 0, s, a);
-    return;
-  }
+  if (tile_rows == kFewRoutes) return launch_few_rows<MODE == kFc1 ? kFc1Few : kFc2Few>(a, a.routes, s);
+  if (tile_rows == 16) return launch_few_rows<MODE>(a, a.max_gtiles, s);
   const int ct = (a.N + 127) / 128;
   const dim3 g((a.max_gtiles + 7) / 8 * 8 * ct);
   if (scales_aligned(a)) hipLaunchKernelGGL((k_mxfp4_tile_grouped<MODE, true>), g, dim3(256), 0, s, a, ct);
