@@ -15,7 +15,7 @@ namespace {
 typedef int i4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 
-enum { kDenseF32 = 0, kDenseBf16 = 1, kFc1 = 2, kFc2 = 3, kFc1Few = 4, kFc2Few = 5 };
+enum { kDenseF32 = 0, kDenseBf16 = 1, kFc1 = 2, kFc2 = 3, kFc1Few = 4, kFc2Few = 5, kFc1FewX = 6 };
 
 // One 128-deep product; byte BYTE of the scale words holds this lane's scales.
 template <int BYTE>
@@ -44,6 +44,36 @@ __device__ __forceinline__ int load_scale_bytes(const uint8_t* p) {
     __builtin_memcpy(&v, p, 4);
     return static_cast<int>(v);
   }
+}
+
+// A block of 32 bf16 values in one lane -> its 32 codes; returns the scale byte.
+__device__ __forceinline__ int quantize_block(const uint4 (&raw)[4], i4v& codes) {
+  uint32_t w[16], m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[4 * i] = raw[i].x;
+    w[4 * i + 1] = raw[i].y;
+    w[4 * i + 2] = raw[i].z;
+    w[4 * i + 3] = raw[i].w;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t lo = (w[i] << 16) & 0x7fffffffu, hi = w[i] & 0x7fff0000u;
+    m = max(m, max(lo, hi));
+  }
+  const uint32_t byte = mxfp4_scale_byte(m);
+  const float inv = mxfp4_inverse_scale(byte);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[4 * i + j] << 16) * inv;
+      v[2 * j + 1] = __uint_as_float(w[4 * i + j] & 0xffff0000u) * inv;
+    }
+    codes[i] = byte == 255u ? 0 : static_cast<int>(mxfp4_codes8(v));
+  }
+  return static_cast<int>(byte);
 }
 
 // Four neighbouring columns col.. of a row of N, at element `at` of y; columns past N are dropped. QUADS: N
@@ -121,9 +151,13 @@ __device__ __forceinline__ void store_swiglu(const f4 (&g)[2], const f4 (&u)[2],
 // the routes of that route's expert itself, one id a thread, and goes on if it is the 1st, 17th, ... of them,
 // with the 16 from there on; slots are the routes. That saves the route map's launch (5.8 us of 35 at T = 16,
 // k = 8, E = 96, H = 1024, I = 512).
+//
+// kFc1FewX: the input is bf16 and each workgroup quantises its tokens' rows itself, a block a lane, while the
+// weights are on their way: another launch less (2.5 us), for rows of one batch (kQuantizeInPlaceMax).
 template <int MODE, int MT, int NT, int KW, int AH, bool TWO>
-__global__ __launch_bounds__(64 * KW, TWO ? 2 : 5) void k_mxfp4_rows(Mxfp4GemmArgs a) {
-  constexpr bool FC1 = MODE == kFc1 || MODE == kFc1Few, FEW = MODE == kFc1Few || MODE == kFc2Few;
+__global__ __launch_bounds__(64 * KW, TWO ? 2 : MODE == kFc1FewX ? 4 : 5) void k_mxfp4_rows(Mxfp4GemmArgs a) {
+  constexpr bool QX = MODE == kFc1FewX, FC1 = MODE == kFc1 || MODE == kFc1Few || QX;
+  constexpr bool FEW = MODE == kFc1Few || MODE == kFc2Few || QX;
   static_assert(!FC1 || (NT == 4 && MT == 1), "first product: two gate and two up fragments");
   static_assert(!FEW || (KW * 64 == kFewRoutesMax && MT == 1), "one id a thread, tiles of 16 routes");
   __shared__ int list[FEW ? kFewRoutesMax : 1];
@@ -210,6 +244,15 @@ __global__ __launch_bounds__(64 * KW, TWO ? 2 : 5) void k_mxfp4_rows(Mxfp4GemmAr
   };
   __shared__ f4 part[KW][MT * NT][64];
   Batch b0, b1;
+  uint4 raw[QX ? AH : 1][4];                     // kFc1FewX: the lane's blocks of its token's row, in flight
+  if constexpr (QX) {
+    const int blk = 4 * AH * wv + AH * q;
+    const uint16_t* row = a.x + static_cast<long long>(list[row0 + min(r, nrows - 1)] / a.top_k) * a.K;
+#pragma unroll
+    for (int u = 0; u < AH; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[u][i] = reinterpret_cast<const uint4*>(row)[4 * min(blk + u, nblk - 1) + i];
+  }
   load_w(wv, b0);
   long long slot[MT];
 #pragma unroll
@@ -221,7 +264,16 @@ __global__ __launch_bounds__(64 * KW, TWO ? 2 : 5) void k_mxfp4_rows(Mxfp4GemmAr
     xq[m] = a.xq + row * (a.K / 2);
     xs[m] = a.xs + row * nblk;
   }
-  load_x(wv, b0);
+  if constexpr (QX) {
+    b0.xs[0] = 0;
+#pragma unroll
+    for (int u = 0; u < AH; ++u) {
+      const int byte = quantize_block(raw[u], b0.x[u][0]);
+      b0.xs[0] |= 4 * AH * wv + AH * q + u < nblk ? byte << (8 * u) : 0;
+    }
+  } else {
+    load_x(wv, b0);
+  }
   f4 acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -236,7 +288,9 @@ __global__ __launch_bounds__(64 * KW, TWO ? 2 : 5) void k_mxfp4_rows(Mxfp4GemmAr
         for (int n = 0; n < NT; ++n) acc[m][n] = mma(u, b.w[u][n], b.ws[n], b.x[u][m], b.xs[m], acc[m][n]);
   };
   int at = wv;                                   // the batch in b0
-  if constexpr (TWO) {
+  if constexpr (QX) {
+    if (at < batches) multiply(b0);              // K <= 128 AH KW: there is no other batch
+  } else if constexpr (TWO) {
     for (; at + KW < batches; at += 2 * KW) {
       load_w(at + KW, b1);
       load_x(at + KW, b1);
@@ -792,7 +846,17 @@ void launch_few_rows(const Mxfp4GemmArgs& a, int tiles, hipStream_t s) {
 
 template <int MODE>
 void launch_grouped(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) {
-  if (tile_rows == kFewRoutes) return launch_few_rows<MODE == kFc1 ? kFc1Few : kFc2Few>(a, a.routes, s);
+  if (tile_rows == kFewRoutes) {
+    if constexpr (MODE == kFc1) {
+      if (a.x) {
+        const dim3 g(a.N / 64 * a.routes), b(256);
+        if (a.K <= 512) hipLaunchKernelGGL((k_mxfp4_rows<kFc1FewX, 1, 4, 4, 1, false>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((k_mxfp4_rows<kFc1FewX, 1, 4, 4, 2, false>), g, b, 0, s, a);
+        return;
+      }
+    }
+    return launch_few_rows<MODE == kFc1 ? kFc1Few : kFc2Few>(a, a.routes, s);
+  }
   if (tile_rows == 16) return launch_few_rows<MODE>(a, a.max_gtiles, s);
   const int ct = (a.N + 127) / 128;
   const dim3 g((a.max_gtiles + 7) / 8 * 8 * ct);

@@ -107,6 +107,7 @@ struct Mxfp4DequantArgs {
 // Grouped: tile i of the list holds rows [y, y + z) (slots) of expert x; X row of a slot:
 // sorted[slot] / top_k (first product) or the slot itself (second).
 struct Mxfp4GemmArgs {
+  const uint16_t* x;         // first product of few routes, K <= kQuantizeInPlaceMax: bf16 [T][K] instead of xq, xs
   const uint8_t* xq;         // [rows][K / 2]
   const uint8_t* xs;         // [rows][K / 32]
   const uint8_t* wq;         // [N][K / 2] (times experts)
@@ -148,5 +149,6 @@ void launch_mxfp4_combine(const Mxfp4CombineArgs& a, int y_dtype, hipStream_t s)
 int mxfp4_tile_rows(long long routes, int experts);
 constexpr int kFewRoutes = 1;
 constexpr int kFewRoutesMax = 256;               // one id a thread
+constexpr int kQuantizeInPlaceMax = 1024;
 
 }  // namespace tmoe

@@ -229,7 +229,10 @@ tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t p, const void* x, const void* i
   g.bq = at<uint8_t>(scratch, p->bq);
   g.bs = at<uint8_t>(scratch, p->bs);
 
+  if (rows == kFewRoutes && p->H <= kQuantizeInPlaceMax) g.x = static_cast<const uint16_t*>(x);
+
   Mxfp4GemmArgs h = g;
+  h.x = nullptr;
   h.xq = g.bq;
   h.xs = g.bs;
   h.wq = wt->w2;
@@ -251,8 +254,8 @@ tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t p, const void* x, const void* i
   c.y = y;
 
   (void)hipGetLastError();
-  if (rows == kFewRoutes) launch_mxfp4_quantize(q, TMOE_BF16, s);
-  else launch_route_map_mxfp4(m, q, s);
+  if (rows != kFewRoutes) launch_route_map_mxfp4(m, q, s);
+  else if (!g.x) launch_mxfp4_quantize(q, TMOE_BF16, s);
   launch_mxfp4_fc1(g, rows, s);
   launch_mxfp4_fc2(h, rows, s);
   launch_mxfp4_combine(c, p->y_dtype, s);

@@ -121,6 +121,8 @@ class ExpertPlan:
         self.handle, self.scratch_bytes = handle, sb.value
         self.hidden, self.inter, self.num_experts, self.top_k = hidden, inter, num_experts, top_k
         self.max_tokens, self.ids_dtype, self.out_dtype = max_tokens, ids_dtype, out_dtype
+        E, H, I = num_experts, hidden, inter
+        self._weight_shapes = ((E, 2 * I, H // 2), (E, 2 * I, H // 32), (E, H, I // 2), (E, H, I // 32))
 
     def close(self):
         if getattr(self, "handle", None) and self.handle.value:
@@ -142,8 +144,16 @@ class ExpertPlan:
         T = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else -1
         if y is None and isinstance(x, torch.Tensor):
             y = torch.empty((max(T, 0), self.hidden), dtype=self.out_dtype, device=x.device)
-        self.check_call(x, ids, w, weights, scratch, y)
-        _launch(x.device.index, lib.tmoe_forward_mxfp4, "tmoe_forward_mxfp4", self.handle, x.data_ptr(), ids.data_ptr(),
+        if not (0 <= T <= self.max_tokens and x.shape[1] == self.hidden and x.dtype in _BITS16 and x.is_contiguous()
+                and _fits(ids, (T, self.top_k), self.ids_dtype) and _fits(w, (T, self.top_k), torch.float32)
+                and _fits(y, (T, self.hidden), self.out_dtype) and isinstance(weights, ExpertWeights)
+                and all(_fits(t, s, torch.uint8) for t, s in zip((weights.w1, weights.s1, weights.w2, weights.s2),
+                                                                 self._weight_shapes))
+                and isinstance(scratch, torch.Tensor) and scratch.dtype is torch.uint8 and scratch.dim() == 1
+                and scratch.is_contiguous() and scratch.numel() >= self.scratch_bytes
+                and _one_gpu(x, ids, w, y, scratch, weights.w1, weights.s1, weights.w2, weights.s2)):
+            self.check_call(x, ids, w, weights, scratch, y)
+        _launch(x.get_device(), lib.tmoe_forward_mxfp4, "tmoe_forward_mxfp4", self.handle, x.data_ptr(), ids.data_ptr(),
                 w.data_ptr(), T, ctypes.byref(weights.c), y.data_ptr(), scratch.data_ptr(), scratch.numel())
         return y
 
@@ -155,15 +165,14 @@ class ExpertPlan:
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"x: {T} tokens, the plan holds at most {self.max_tokens}")
-        H, I, E, k = self.hidden, self.inter, self.num_experts, self.top_k
+        H, k = self.hidden, self.top_k
         _require(x, "x", (T, H), _BITS16)
         _require(ids, "ids", (T, k), (self.ids_dtype,))
         _require(w, "w", (T, k), (torch.float32,))
         _require(y, "y", (T, H), (self.out_dtype,))
         if not isinstance(weights, ExpertWeights):
             raise ValueError("weights: expected ExpertWeights")
-        for name, shape in (("w1", (E, 2 * I, H // 2)), ("s1", (E, 2 * I, H // 32)), ("w2", (E, H, I // 2)),
-                            ("s2", (E, H, I // 32))):
+        for name, shape in zip(ExpertWeights.FIELDS, self._weight_shapes):
             _require(getattr(weights, name), name, shape, (torch.uint8,))
         _check_scratch(scratch, self.scratch_bytes)
         _same_device([("x", x), ("ids", ids), ("w", w), ("y", y), ("scratch", scratch)]
