@@ -225,6 +225,46 @@ def test_layer(T, H, I, E, k, dtype):
     c.check(y)
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [(40, 160, 96, 64, 8), (35, 1056, 64, 70, 8), (60, 64, 1088, 40, 6),   # 16-row tiles
+                                       (300, 672, 96, 4, 2), (200, 96, 640, 5, 2), (130, 512, 544, 3, 2),
+                                       (8, 64, 32, 40, 32), (90, 64, 64, 33, 32)])
+def test_layer_other_forms(T, H, I, E, k):
+    """Routes between the layer's forms, rows of 17 to 34 blocks, the largest top-k."""
+    say(f"[case] MXFP4 layer T={T} H={H} I={I} E={E} k={k}")
+    c = Layer(T, H, I, E, k, drop=0.1)
+    y = torch.full((T, H), float("nan"), device="cuda")
+    c.run(y)
+    c.check(y)
+
+
+@pytest.mark.parametrize("T,k", [(20, 3), (85, 3), (256, 1)])
+def test_layer_few_routes_one_expert_dropped_and_repeated(T, k):
+    """Up to 256 routes without a route map: many routes of one expert, ids outside, the same id twice."""
+    c = Layer(T, 128, 96, 60, k, ids_dtype=torch.int32)
+    c.ids[:] = 7
+    c.ids[3] = -1
+    c.ids[T // 2:T // 2 + 4, 0] = 60
+    c.ids[-1] = 2 ** 31 - 1
+    c.ids[1, 0] = 59
+    c.dids = _gpu(c.ids).to(torch.int32)
+    c.dw[3] = float("inf")
+    y = torch.full((T, 128), float("nan"), device="cuda")
+    c.run(y)
+    assert torch.all(y[3] == 0) and torch.all(y[-1] == 0)
+    c.check(y)
+
+
+@pytest.mark.parametrize("T,E", [(12, 40), (60, 70), (200, 6)])
+def test_layer_a_token_with_an_infinity_stays_alone(T, E):
+    c = Layer(T, 96, 64, E, 4)
+    good = c.run().clone()
+    c.dx[5, 40], c.dx[9, 3] = float("inf"), float("nan")
+    y = c.run()
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[5] = bad[9] = True
+    assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], good[~bad])
+
+
 def test_layer_uneven_routes_and_dropped_ids():
     c = Layer(260, 256, 128, 40, 6, skew=True, drop=0.2, max_tokens=300)
     c.ids[7] = -1                                       # a token without any expert

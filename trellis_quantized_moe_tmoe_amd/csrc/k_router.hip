@@ -245,16 +245,16 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_rows(BalanceArgs
 }
 
 // Balance loss, launch 2 (one workgroup): totals over the groups, then the loss and its slope for each
-// expert. A thread adds four experts' sums of every (1024 / (pitch / 4))-th group, so a launch has all
+// expert. A thread adds four experts' sums of every (1024 / (pitch / 4))-th group (64th at most), so a launch has all
 // its loads in flight in a few rounds (one thread per expert walking 512 groups took 128 us); the order
 // of the sums is fixed and they are held in 64 bits.
 __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a) {
-  __shared__ double pt[1024 * 4];
+  __shared__ double pt[1024 * 4];               // [per][pitch], per * pitch <= 4096
   __shared__ int ct[1024 * 4];
   __shared__ int nred[16], cred[16];
   __shared__ double lred[16];
   const int tid = threadIdx.x, E = a.experts, quads = a.pitch / 4;
-  const int per = 1024 / quads;                  // thread rows
+  const int per = min(1024 / quads, 64);         // thread rows (more would only lengthen their join)
   const int row = tid / quads, col = tid % quads;
   double p[4] = {0, 0, 0, 0};
   int c[4] = {0, 0, 0, 0};
