@@ -26,9 +26,7 @@ struct BF16 {
   typedef uint16_t T;
   static __device__ __forceinline__ float get(uint16_t v) { return bf16_to_f32(v); }
   static __device__ __forceinline__ uint16_t put(float v) {   // round to nearest even, NaN kept
-    const uint32_t u = __float_as_uint(v);
-    if ((u & 0x7fffffffu) > 0x7f800000u) return static_cast<uint16_t>((u >> 16) | 0x40u);
-    return static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
   }
 };
 struct F16 {
@@ -109,7 +107,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // expert that has it (one ballot per register; registers hold ascending experts), then that entry's key
 // is cleared. Key 0 marks an expert that is not available (-inf, NaN or past E). A selected logit is its
 // key read back, so the weights need no gather. The vector unit bounds it. Two rows a wavefront, side by
-// side, measured the same (14.7 us at T = 16384, E = 256, k = 8).
+// side, measured the same (14 us at T = 16384, E = 256, k = 8).
 template <class D, int V>
 __global__ __launch_bounds__(64 * kWavesPerGroup) void k_router_topk(RouterTopkArgs a) {
   const int lane = threadIdx.x & 63;
@@ -237,51 +235,51 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_rows(BalanceArgs
     a.psum[static_cast<long long>(blockIdx.x) * a.pitch + e] = p;
     a.csum[static_cast<long long>(blockIdx.x) * a.pitch + e] = cs[e];
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 64) {                        // rows that count, and routes
     int c = 0;
-    for (int q = 0; q < kBalanceWaves; ++q) c += ns[q];
-    a.nsum[blockIdx.x] = c;
+    for (int e = lane; e < E; e += 64) c += cs[e];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) c += __shfl_xor(c, d, 64);
+    if (lane == 0) {
+      int rows = 0;
+      for (int q = 0; q < kBalanceWaves; ++q) rows += ns[q];
+      a.nsum[2 * blockIdx.x] = rows;
+      a.nsum[2 * blockIdx.x + 1] = c;
+      if (blockIdx.x == 0) *a.done = 0;          // the second launch's counter
+    }
   }
 }
 
-// Balance loss, launch 2 (one workgroup): totals over the groups, then the loss and its slope for each
-// expert. A thread adds four experts' sums of every (1024 / (pitch / 4))-th group (64th at most), so a launch has all
-// its loads in flight in a few rounds (one thread per expert walking 512 groups took 128 us); the order
-// of the sums is fixed and they are held in 64 bits.
-__global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a) {
-  __shared__ double pt[1024 * 4];               // [per][pitch], per * pitch <= 4096
-  __shared__ int ct[1024 * 4];
-  __shared__ int nred[16], cred[16];
-  __shared__ double lred[16];
+// Balance loss, launch 2: a workgroup adds up 32 experts over the groups, each thread four experts of every 32nd
+// group, so that all its loads are in flight at once (one thread an expert walking 512 groups took 128 us,
+// one workgroup for all experts 8.6 us at 256 groups, E = 256; 5.4 us here). The order of the sums is fixed and they are
+// held in 64 bits; the workgroup that ends last adds the others' parts of the loss, in order.
+__global__ __launch_bounds__(256) void k_balance_finish(BalanceArgs a) {
+  __shared__ double pt[32][33];
+  __shared__ int ct[32][33];
+  __shared__ int nred[4], cred[4];
   const int tid = threadIdx.x, E = a.experts, quads = a.pitch / 4;
-  const int per = min(1024 / quads, 64);         // thread rows (more would only lengthen their join)
-  const int row = tid / quads, col = tid % quads;
+  const int row = tid / 8, col = blockIdx.x * 8 + tid % 8;
   double p[4] = {0, 0, 0, 0};
-  int c[4] = {0, 0, 0, 0};
-  if (row < per) {
+  int c[4] = {0, 0, 0, 0}, n = 0, all = 0;
+  if (col < quads) {
 #pragma unroll 8
-    for (int g = row; g < a.groups; g += per) {
+    for (int g = row; g < a.groups; g += 32) {
       const float4 x = reinterpret_cast<const float4*>(a.psum)[static_cast<long long>(g) * quads + col];
       const int4 y = reinterpret_cast<const int4*>(a.csum)[static_cast<long long>(g) * quads + col];
       p[0] += x.x; p[1] += x.y; p[2] += x.z; p[3] += x.w;
       c[0] += y.x; c[1] += y.y; c[2] += y.z; c[3] += y.w;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      pt[row * a.pitch + 4 * col + i] = p[i];
-      ct[row * a.pitch + 4 * col + i] = c[i];
-    }
   }
-  int n = tid < a.groups ? a.nsum[tid] : 0;
-  __syncthreads();
-  double pe = 0.0;
-  int ce = 0;
-  if (tid < E)
-    for (int r = 0; r < per; ++r) {
-      pe += pt[r * a.pitch + tid];
-      ce += ct[r * a.pitch + tid];
-    }
-  int all = ce;
+  for (int g = tid; g < a.groups; g += 256) {
+    n += a.nsum[2 * g];
+    all += a.nsum[2 * g + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    pt[row][4 * (tid % 8) + i] = p[i];
+    ct[row][4 * (tid % 8) + i] = c[i];
+  }
 #pragma unroll
   for (int d = 32; d; d >>= 1) {
     n += __shfl_xor(n, d, 64);
@@ -292,26 +290,39 @@ __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a) {
     cred[tid >> 6] = all;
   }
   __syncthreads();
-  int nt = 0, total = 0;
+  const int nt = nred[0] + nred[1] + nred[2] + nred[3], total = cred[0] + cred[1] + cred[2] + cred[3];
+  if (tid < 64) {
+    const int e = blockIdx.x * 32 + tid;
+    double l = 0.0;
+    if (tid < 32 && e < E) {
+      double pe = 0.0;
+      int ce = 0;
+      for (int r = 0; r < 32; ++r) {
+        pe += pt[r][tid];
+        ce += ct[r][tid];
+      }
+      const double f = total > 0 ? static_cast<double>(ce) / total : 0.0;
+      const double slope = nt > 0 ? static_cast<double>(a.coefficient) * E * f / nt : 0.0;
+      a.counts[e] = ce;
+      a.slope[e] = static_cast<float>(slope);
+      l = slope * pe;
+    }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    nt += nred[i];
-    total += cred[i];
-  }
-  const double f = total > 0 ? static_cast<double>(ce) / total : 0.0;
-  const double slope = nt > 0 ? static_cast<double>(a.coefficient) * E * f / nt : 0.0;
-  double l = tid < E ? slope * pe : 0.0;
-  for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d, 64);
-  if ((tid & 63) == 0) lred[tid >> 6] = l;
-  __syncthreads();
-  if (tid < E) {
-    a.counts[tid] = ce;
-    a.slope[tid] = static_cast<float>(slope);
-  }
-  if (tid == 0) {
-    double s = 0.0;
-    for (int i = 0; i < 16; ++i) s += lred[i];
-    *a.loss = static_cast<float>(s);
+    for (int d = 16; d; d >>= 1) l += __shfl_xor(l, d, 64);
+    if (tid == 0) {
+      const int parts = gridDim.x;
+      if (parts == 1 || a.groups == 0) {         // no groups: nothing cleared the counter, every part is 0
+        *a.loss = static_cast<float>(l);
+      } else {
+        __hip_atomic_store(a.part + blockIdx.x, l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const bool last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+        if (last) {
+          double s = 0.0;
+          for (int i = 0; i < parts; ++i) s += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          *a.loss = static_cast<float>(s);
+        }
+      }
+    }
   }
 }
 
@@ -422,7 +433,7 @@ void launch_balance(const BalanceArgs& a, int dtype, hipStream_t s) {
                            dim3(64 * kBalanceWaves), 0, s, a);
       });
     });
-  hipLaunchKernelGGL(k_balance_finish, dim3(1), dim3(1024), 0, s, a);
+  hipLaunchKernelGGL(k_balance_finish, dim3((a.experts + 31) / 32), dim3(256), 0, s, a);
 }
 
 void launch_router_grad(const RouterGradArgs& a, int dtype, hipStream_t s) {

@@ -27,7 +27,9 @@ struct BalanceArgs {
   int pitch;                 // E rounded up to a multiple of 4
   float* psum;               // [groups][pitch] sums of probabilities
   int32_t* csum;             // [groups][pitch] routes per expert
-  int32_t* nsum;             // [groups] rows that count
+  int32_t* nsum;             // [groups][2] rows that count, and routes
+  int32_t* done;             // workgroups of the second launch that have ended (cleared by the first)
+  double* part;              // [ceil(E / 32)] their parts of the loss
   float* loss;               // [1]
   int32_t* counts;           // [E]
   float* slope;              // [E] dloss/dp_te = coefficient * E * f_e / n
@@ -46,7 +48,7 @@ struct RouterGradArgs {
   void* dlogits;             // [T][E], the logits' type
 };
 
-constexpr int kBalanceMaxGroups = 256;   // one workgroup of 16 wavefronts a CU (at most 1024: the second launch's threads)
+constexpr int kBalanceMaxGroups = 256;   // one workgroup of 16 wavefronts a CU
 
 // dtype: TMOE_F32, TMOE_BF16 or TMOE_F16
 void launch_router_topk(const RouterTopkArgs& a, int dtype, hipStream_t s);

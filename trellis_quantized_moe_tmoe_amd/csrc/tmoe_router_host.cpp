@@ -42,7 +42,7 @@ tmoe_status check_rows(const tmoe_router_config* c, const void* logits, int64_t 
 
 struct BalanceShape {
   int groups, rows, pitch;
-  size_t psum, csum, nsum, total;                // arena offsets
+  size_t psum, csum, nsum, done, part, total;    // arena offsets
 };
 
 BalanceShape balance_shape(int T, int E) {
@@ -55,7 +55,9 @@ BalanceShape balance_shape(int T, int E) {
   b.psum = 0;
   b.csum = up(4ull * b.groups * b.pitch);
   b.nsum = b.csum + up(4ull * b.groups * b.pitch);
-  b.total = b.nsum + up(4ull * b.groups);
+  b.done = b.nsum + up(8ull * b.groups);
+  b.part = b.done + up(4);
+  b.total = b.groups ? b.part + up(8ull * ((E + 31) / 32)) : 0;
   return b;
 }
 
@@ -127,6 +129,8 @@ tmoe_status tmoe_balance_loss(const tmoe_router_config* c, const void* logits, i
   a.psum = reinterpret_cast<float*>(base + b.psum);
   a.csum = reinterpret_cast<int32_t*>(base + b.csum);
   a.nsum = reinterpret_cast<int32_t*>(base + b.nsum);
+  a.done = reinterpret_cast<int32_t*>(base + b.done);
+  a.part = reinterpret_cast<double*>(base + b.part);
   a.loss = loss;
   a.counts = counts;
   a.slope = slope;
