@@ -322,7 +322,7 @@ typedef struct {
   int32_t inter;               /* I: multiple of 32, 32..8192                                   */
   int32_t num_experts;         /* E: 1..512                                                     */
   int32_t top_k;               /* k: 1..32                                                      */
-  int32_t max_tokens;          /* capacity T_max >= 1; T*k <= 2^22                              */
+  int32_t max_tokens;          /* capacity T_max >= 1; T*k <= 2^22, T*H <= 2^33                 */
   int32_t ids_dtype;           /* TMOE_IDS_I32 or TMOE_IDS_I64                                   */
   int32_t y_dtype;             /* TMOE_F32 or TMOE_BF16                                          */
 } tmoe_mxfp4_config;

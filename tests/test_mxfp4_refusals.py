@@ -131,3 +131,24 @@ def test_reference_by_hand():
     bad[7] = np.inf
     assert M.quantize(bad)[1].tolist() == [255] and not M.quantize(bad)[0].any()
     assert np.array_equal(M.unpack(M.pack(code)), code)
+
+
+def test_sizes_past_what_a_launch_or_an_argument_holds():
+    """A plan of more than 2^33 input values (the weighted sum's threads), and sizes that lose their high bits in a
+    32-bit argument: 2^32 + 64 must not pass for 64."""
+    from trellis_quantized_moe_tmoe_amd import mxfp4, native
+    h = ctypes.c_void_p()
+    for T, H, want in [(1 << 20, 8192, 0), ((1 << 20) + 1, 8192, 2), (1 << 22, 2048, 0), (1 << 22, 2080, 2)]:
+        cfg = native.Mxfp4Config(H, 32, 4, 1, T, native.IDS_I32, native.F32)
+        assert native.lib.tmoe_mxfp4_plan(ctypes.byref(cfg), ctypes.byref(h), None) == want
+        if want == 0:
+            native.lib.tmoe_mxfp4_plan_destroy(h)
+    big = 2 ** 32 + 64
+    m = lambda *s: torch.empty(*s, dtype=torch.uint8, device="meta")  # noqa: E731
+    for bad in [lambda: mxfp4.quantize(torch.empty(1, big, device="meta")),
+                lambda: mxfp4.dequantize(m(1, big // 2), m(1, big // 32)),
+                lambda: mxfp4.linear(m(big, 32), m(big, 2), m(6, 32), m(6, 2)),
+                lambda: mxfp4.linear(m(6, 32), m(6, 2), m(big, 32), m(big, 2)),
+                lambda: mxfp4.ExpertPlan(big, 32, 4, 2, 8), lambda: mxfp4.ExpertPlan(64, 32, 4, 2, big)]:
+        with pytest.raises(ValueError, match="out of range"):
+            bad()

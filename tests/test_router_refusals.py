@@ -118,3 +118,13 @@ def test_reference_by_hand():
     ids = np.arange(16).reshape(4, 4) % 8
     loss, c, _, _ = R.balance(np.zeros((4, 8)), np.ones(4, bool), ids, 0.25)
     assert c.tolist() == [2] * 8 and np.isclose(loss, 0.25)
+
+
+def test_sizes_past_32_bits():
+    """2^32 + 5 rows or experts must not pass for 5."""
+    from trellis_quantized_moe_tmoe_amd import router
+    big = 2 ** 32 + 5
+    for l, k in [(torch.empty(big, 8, device="meta"), 2), (torch.empty(8, big, device="meta"), 2),
+                 (torch.empty(8, 8, device="meta"), 2 ** 32 + 2)]:
+        with pytest.raises(ValueError, match="out of range"):
+            router.topk(l, k)

@@ -21,8 +21,7 @@ __device__ __forceinline__ uint32_t mxfp4_scale_byte(uint32_t amax_bits) {
   return static_cast<uint32_t>(byte > 0 ? byte : 0);
 }
 
-// 2^-(byte - 127), exact for every byte below 255; 0 for 255, so that block's codes come out as zeros
-// of either sign or (0 * inf) are replaced by the caller.
+// 2^-(byte - 127), exact for the bytes above (0..253); for 255 the caller puts zeros in place of the codes.
 __device__ __forceinline__ float mxfp4_inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
 // 2^(byte - 127); NaN for 255.

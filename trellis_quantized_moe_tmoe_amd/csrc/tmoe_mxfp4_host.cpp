@@ -29,6 +29,7 @@ constexpr int kMaxDim = 8192;                    // of the layer
 constexpr int kMaxLinearDim = 1 << 16;
 constexpr int kMaxLinearTokens = 1 << 20;
 constexpr long long kMaxRoutes = 1LL << 22;
+constexpr long long kMaxValues = 1LL << 33;      // T * H: the weighted sum has a thread for four, a launch fewer than 2^32
 constexpr int kBlockM = 64;                      // rows of the route map's own tile table (not read here)
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -116,7 +117,7 @@ tmoe_status tmoe_mxfp4_plan(const tmoe_mxfp4_config* c, tmoe_mxfp4_plan_t* out, 
   if (!dim_ok(c->hidden) || !dim_ok(c->inter)) return TMOE_ERR_UNSUPPORTED;
   if (c->num_experts > kMaxExperts || c->top_k > kMaxTopK) return TMOE_ERR_UNSUPPORTED;
   const long long R = static_cast<long long>(c->max_tokens) * c->top_k;
-  if (R > kMaxRoutes) return TMOE_ERR_UNSUPPORTED;
+  if (R > kMaxRoutes || static_cast<long long>(c->max_tokens) * c->hidden > kMaxValues) return TMOE_ERR_UNSUPPORTED;
   tmoe_mxfp4_plan_s* p = new (std::nothrow) tmoe_mxfp4_plan_s();
   if (!p) return TMOE_ERR_INVALID_ARG;
   p->H = c->hidden;

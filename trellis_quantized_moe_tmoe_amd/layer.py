@@ -59,6 +59,13 @@ def _fits(t, shape, dtype) -> bool:
     return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
+def _int32(**sizes) -> None:
+    """Raise ValueError for a size that the library's 32-bit arguments cannot hold (ctypes would cut it off)."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"{name}: {n} is out of range")
+
+
 def _one_gpu(first, *others) -> bool:
     index = first.get_device()
     if not first.is_cuda:

@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from . import native
-from .layer import _BITS16, _check_scratch, _fits, _launch, _one_gpu, _require, _same_device
+from .layer import _BITS16, _check_scratch, _fits, _int32, _launch, _one_gpu, _require, _same_device
 from .native import check, lib
 
 _DTYPES = {torch.float32: native.F32, torch.bfloat16: native.BF16, torch.float16: native.F16}
@@ -34,6 +34,7 @@ def quantize(x: torch.Tensor):
         _require(x, "x", x.shape, tuple(_DTYPES))
     if K == 0 or K % 32:
         raise ValueError(f"x: the last dimension is {K}, expected a multiple of 32")
+    _int32(K=K)
     if not x.is_cuda:
         _same_device([("x", x)])
     dev = x.device
@@ -52,6 +53,10 @@ def _operand(codes, scales, name: str, dim: Optional[int] = None) -> int:
     K = 2 * shape[-1]
     if K == 0 or K % 32:
         raise ValueError(f"{name}: rows of {K} values, expected a multiple of 32")
+    if dim == 2:
+        _int32(K=K, rows=shape[0])
+    else:
+        _int32(K=K)
     if not (codes.dtype is torch.uint8 and codes.is_contiguous()):
         _require(codes, f"{name} codes", shape, (torch.uint8,))
     if not _fits(scales, (*shape[:-1], K // 32), torch.uint8):
@@ -113,6 +118,7 @@ class ExpertPlan:
                  out_dtype=torch.float32):
         if ids_dtype not in (torch.int32, torch.int64):
             raise ValueError(f"ids_dtype: {ids_dtype}, expected torch.int32 or torch.int64")
+        _int32(hidden=hidden, inter=inter, num_experts=num_experts, top_k=top_k, max_tokens=max_tokens)
         self.config = native.Mxfp4Config(hidden, inter, num_experts, top_k, max_tokens,
                                          native.IDS_I64 if ids_dtype == torch.int64 else native.IDS_I32,
                                          _out_dtype(out_dtype))

@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import native
-from .layer import _fits, _launch, _one_gpu, _require, _same_device
+from .layer import _fits, _int32, _launch, _one_gpu, _require, _same_device
 from .native import check, lib
 
 _DTYPES = {torch.float32: native.F32, torch.bfloat16: native.BF16, torch.float16: native.F16}
@@ -43,6 +43,8 @@ def _config(logits, top_k: int, ids_dtype, renormalize: bool):
     if logits.dtype not in _DTYPES:
         raise ValueError(f"logits: dtype {logits.dtype}, expected one of {[str(d) for d in _DTYPES]}")
     (T, E), (row, step) = logits.shape, logits.stride()
+    if T + E + abs(top_k) >= 2 ** 31:
+        _int32(T=T, E=E, top_k=top_k)
     if T > 0 and ((E > 1 and step != 1) or (T > 1 and row < E)):
         raise ValueError("logits: the values of a row must be adjacent and rows must not overlap")
     if ids_dtype not in _IDS:
