@@ -289,6 +289,19 @@ def test_layer_large_batch_many_routes():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("T,H,I,E,k,skew", [(500, 640, 2048, 10, 4, False), (1300, 1152, 2080, 6, 1, False),
+                                            (900, 1024, 1536, 12, 3, True)])
+def test_layer_more_tiles_than_workgroups(T, H, I, E, k, skew):
+    """The first product's workgroups take several tiles each: rows of whole and of part groups of scales, an odd
+    number of groups, top-1, a last column block that is not full, dropped routes; and the same bits again."""
+    say(f"[case] MXFP4 layer T={T} H={H} I={I} E={E} k={k} skew={skew}")
+    c = Layer(T, H, I, E, k, skew=skew, drop=0.2 if skew else 0.0)
+    y = torch.full((T, H), float("nan"), device="cuda")
+    c.run(y)
+    c.check(y)
+    assert torch.equal(c.run(), y)
+
+
 def test_layer_zero_tokens_and_smaller_batches():
     c = Layer(40, 128, 64, 6, 2, max_tokens=64)
     y = torch.full((0, 128), 1.0, device="cuda")

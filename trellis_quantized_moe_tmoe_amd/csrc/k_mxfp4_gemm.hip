@@ -5,6 +5,8 @@
 // l holds row (or column) l % 16, block l / 16 of the 128-deep step (16 bytes, as stored) and its scale
 // byte. The weights are the first operand, so a lane's four results are four neighbouring output columns
 // (4 (l / 16) + i) of one token (l % 16). Products are exact; sums are fp32.
+#include <type_traits>
+
 #include "tmoe.h"
 #include "tmoe_mxfp4.hpp"
 
@@ -419,43 +421,80 @@ __device__ __forceinline__ void store_swiglu32(const f16v& g, const f16v& u, uin
 // ALIGNED: K is a multiple of 128 and at least 512 and the scales are 4-byte aligned. Their rows are then copied
 // straight to LDS like the codes; else they pass through registers, where the compiler's wait for them is one
 // for every copy in flight.
-template <int MODE, int WT, int WC, int MT, int NT, bool ALIGNED>
-__device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expert, int row0, int nrows, int cg,
-                                          uint8_t* lds) {
+//
+// next: gives the workgroup's next tile, until there is none (NoNext: at once). The ring does not stop between two
+// tiles: the copies of a tile's last group are the first two pairs of the next tile, and land while the results
+// are stored.
+struct TileAt {
+  long long expert;
+  int row0, nrows, cg;
+};
+struct NoNext {
+  __device__ bool operator()(TileAt&) const { return false; }
+};
+
+template <int MODE, int WT, int WC, int MT, int NT, bool ALIGNED, class Next>
+__device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, TileAt t, Next next, uint8_t* lds) {
+  constexpr bool STREAM = !std::is_same<Next, NoNext>::value;
+  static_assert((ALIGNED && MODE == kFc1) || !STREAM, "its scales are copies and its results need no LDS");
   using S = Tile<MODE, WT, WC, MT, NT>;
   static_assert(WT * WC == 4 && (MODE != kFc1 || NT == 2), "four wavefronts; first product: gate and up fragment");
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r32 = lane & 31, h = lane >> 5;
   const int wt = wv / WC, wc = wv % WC;
   const int nblk = a.K / 32, steps = (nblk + 3) / 4;
-  const uint8_t* wq = a.wq + expert * a.N * (a.K / 2);
-  const uint8_t* ws = a.ws + expert * a.N * nblk;
   const int inter = a.N / 2;
 
-  // global row of a tile row i: tokens first, then weight rows; rows past the end repeat the last one
-  auto source = [&](int i, bool scales) -> const uint8_t* {
-    if (i < S::TR) {
-      long long row = row0 + min(i, nrows - 1);
-      if constexpr (MODE == kFc1) row = a.sorted[row] / a.top_k;
-      return scales ? a.xs + row * nblk : a.xq + row * (a.K / 2);
-    }
-    const int j = i - S::TR;
-    long long col;
-    if constexpr (MODE == kFc1) col = ((j >> 5) & 1) * inter + min(cg * (S::TC / 2) + (j >> 6) * 32 + (j & 31), inter - 1);
-    else col = min(cg * S::TC + j, a.N - 1);
-    return scales ? ws + col * nblk : wq + col * (a.K / 2);
+  // Rows of a tile: tokens first, then weight rows; rows past the end repeat the last one. A token's row of the first
+  // product is behind its route (route_of), which is read apart; route / k by the reciprocal ceil(2^32 / k),
+  // exact for routes below 2^27 (k <= 32).
+  const uint32_t recip = MODE == kFc1 ? 0xffffffffu / static_cast<uint32_t>(a.top_k) + 1u : 0u;   // k = 1: wraps to 0
+  auto route_of = [&](const TileAt& t, int i) -> int {
+    if constexpr (MODE == kFc1) return a.sorted[t.row0 + min(i, t.nrows - 1)];
+    else return 0;
+  };
+  auto token_row = [&](const TileAt& t, int i, int route) -> uint32_t {
+    if constexpr (MODE == kFc1) return __umulhi(static_cast<uint32_t>(route), recip) + (recip ? 0u : route);
+    else return t.row0 + min(i, t.nrows - 1);
+  };
+  auto weight_row = [&](const TileAt& t, int j) -> uint32_t {          // of all experts: below 2^24
+    uint32_t col;
+    if constexpr (MODE == kFc1) col = ((j >> 5) & 1) * inter + min(t.cg * (S::TC / 2) + (j >> 6) * 32 + (j & 31), inter - 1);
+    else col = min(t.cg * S::TC + j, a.N - 1);
+    return static_cast<uint32_t>(t.expert) * a.N + col;
+  };
+  auto scales_at = [&](const TileAt& t, int i, int route) -> const uint8_t* {
+    const bool tok = i < S::TR;
+    const uint32_t row = tok ? token_row(t, i, route) : weight_row(t, i - S::TR);
+    return (tok ? a.xs : a.ws) + static_cast<unsigned long long>(row) * static_cast<uint32_t>(nblk);
   };
   // copies in the order weights, tokens: a token's address may wait for its route
   const uint8_t* src[S::LPP];
   auto place_of = [&](int i) { return wv + 4 * (i < S::TC / 32 ? S::TR / 32 + i : i - S::TC / 32); };
-#pragma unroll
-  for (int i = 0; i < S::LPP; ++i) src[i] = source(8 * place_of(i) + (lane >> 3), false);
+  auto code_row = [&](int i) { return 8 * place_of(i) + (lane >> 3); };
+  auto scale_row = [&](int i) {
+    return ALIGNED ? 64 * min(wv + 4 * i, (S::TR + S::TC) / 64 - 1) + lane : min(tid + 256 * i, S::TR + S::TC - 1);
+  };
   const uint8_t* ssrc[S::SPT];
+  int route[S::LPP], sroute[S::SPT];
+  auto read_routes = [&](const TileAt& t) {
 #pragma unroll
-  for (int i = 0; i < S::SPT; ++i) {
-    if constexpr (ALIGNED) ssrc[i] = source(64 * min(wv + 4 * i, (S::TR + S::TC) / 64 - 1) + lane, true);
-    else ssrc[i] = nblk >= 16 ? source(min(tid + 256 * i, S::TR + S::TC - 1), true) : a.wq;
-  }
+    for (int i = 0; i < S::LPP; ++i) route[i] = i < S::TC / 32 ? 0 : route_of(t, code_row(i));
+#pragma unroll
+    for (int i = 0; i < S::SPT; ++i) sroute[i] = route_of(t, scale_row(i));
+  };
+  auto point_at = [&](const TileAt& t) {
+    const uint32_t pitch = a.K / 2;
+#pragma unroll
+    for (int i = 0; i < S::LPP; ++i) {
+      if (i < S::TC / 32) src[i] = a.wq + static_cast<unsigned long long>(weight_row(t, code_row(i) - S::TR)) * pitch;
+      else src[i] = a.xq + static_cast<unsigned long long>(token_row(t, code_row(i), route[i])) * pitch;
+    }
+#pragma unroll
+    for (int i = 0; i < S::SPT; ++i) ssrc[i] = ALIGNED || nblk >= 16 ? scales_at(t, scale_row(i), sroute[i]) : a.wq;
+  };
+  read_routes(t);
+  point_at(t);
   const int chunk = (lane & 7) ^ swizzle(8 * (wv & 1) + (lane >> 3));
 
   auto issue = [&](int pair, int i) {            // one of a wavefront's LPP copies (8 rows) of a pair of steps
@@ -467,13 +506,14 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
   // Scales of steps 4 g .. 4 g + 3: bytes 16 g .. of each row. The last group's load starts where it ends with
   // the row and is shifted when it is stored; rows shorter than 16 bytes have one
   // group, read before the loop (the loop's fetches then read 16 bytes of codes for nothing).
-  auto copy_scales = [&](int g) {                // ALIGNED: 64 rows of 16 bytes a copy, repeats at the end
+  int buffer = 0;                                // scale buffer of group 0
+  auto copy_scales = [&](int g, int b) {         // ALIGNED: 64 rows of 16 bytes a copy, repeats at the end
     const int from = min(16 * g, nblk - 16);
 #pragma unroll
     for (int i = 0; i < S::SPT; ++i)
       __builtin_amdgcn_global_load_lds(
           (const void __attribute__((address_space(1)))*)(ssrc[i] + from),
-          (void __attribute__((address_space(3)))*)(lds + 2 * S::kSlot + (g & 1) * S::kScales +
+          (void __attribute__((address_space(3)))*)(lds + 2 * S::kSlot + (b & 1) * S::kScales +
                                                     min(wv + 4 * i, (S::TR + S::TC) / 64 - 1) * 1024),
           16, 0, 0);
   };
@@ -513,12 +553,13 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     // rows of less than 16 bytes: 16 bytes that lie in the array, shifted to the row's first and cut behind its last
     const long long tokens = MODE == kFc1 ? a.routes / a.top_k : MODE == kFc2 ? a.routes : a.rows;
     const uint8_t* x_end = a.xs + tokens * nblk;
+    const uint8_t* ws = a.ws + t.expert * a.N * nblk;
     const uint8_t* w_end = ws + static_cast<long long>(a.N) * nblk;    // the expert's own rows
     uint8_t* buf = lds + 2 * S::kSlot;
 #pragma unroll
     for (int i = 0; i < S::SPT; ++i) {
       const int at = min(tid + 256 * i, S::TR + S::TC - 1);
-      const uint8_t* p = source(at, true);
+      const uint8_t* p = scales_at(t, at, route_of(t, at));
       const uint8_t* end = at < S::TR ? x_end : w_end;
       uint32_t w[4] = {0, 0, 0, 0};
       if (end - (at < S::TR ? a.xs : ws) >= 16) {
@@ -559,7 +600,7 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
     const uint8_t* slot = lds + ((ks >> 1) & 1) * S::kSlot + lane_at[2 * (ks & 1) + s];
     // ALIGNED: the last group's bytes start where they end with the row
     const int at = ALIGNED ? min(4 * ks - min(16 * (ks >> 2), nblk - 16), 12) : 4 * (ks & 3);
-    const uint8_t* sc = lds + 2 * S::kSlot + ((ks >> 2) & 1) * S::kScales + 16 * r32 + at + 2 * h;
+    const uint8_t* sc = lds + 2 * S::kSlot + ((buffer + (ks >> 2)) & 1) * S::kScales + 16 * r32 + at + 2 * h;
     if (p < NT) {
       f.w[p] = *reinterpret_cast<const i4v*>(slot + 128 * S::TR + 4096 * (wc * NT + p));
       if (scales) nw[p] = *reinterpret_cast<const uint16_t*>(sc + 16 * S::TR + 512 * (wc * NT + p));
@@ -571,12 +612,8 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
   };
 
   f16v acc[MT][NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[m][n] = f16v{};
 
-  if constexpr (ALIGNED) copy_scales(0);
+  if constexpr (ALIGNED) copy_scales(0, 0);
   else first_scales();
 #pragma unroll
   for (int d = 0; d < 2; ++d)
@@ -596,14 +633,17 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
   // the 32 cycles of the instruction before is lost (four of them behind a bunch of reads and copies: 52.9 us
   // at T = 4096, K = N = 4096; left free, the compiler gathers the matrix instructions of four steps).
   constexpr int MM = MT * NT, RD = MT + NT;
-  auto step = [&](int ks, auto phase) {
+  const int groups = (steps + 3) / 4;            // whole groups of four: steps past K add nothing
+  // LAST: the group's copies are those of the next tile (its pairs 0 and 1, its scale group 0), to which src points
+  auto step = [&](int ks, auto phase, auto last) {
     constexpr int PHASE = decltype(phase)::value;
+    constexpr bool LAST = decltype(last)::value;
     const int mask = !ALIGNED || 4 * ks < nblk ? 0xffff : 0;   // ALIGNED: steps past K read any scale
 #pragma unroll
     for (int m = 0; m < MT; ++m) xs[m] = nx[m] & mask;
 #pragma unroll
     for (int n = 0; n < NT; ++n) ws4[n] = nw[n] & mask;
-    if constexpr (PHASE == 0 && ALIGNED) copy_scales((ks >> 2) + 1);
+    if constexpr (PHASE == 0 && ALIGNED) copy_scales(LAST ? 0 : (ks >> 2) + 1, buffer + (ks >> 2) + 1);
     if constexpr (PHASE == 0 && !ALIGNED) load_scales((ks >> 2) + 1);
     if constexpr (PHASE == 2 && !ALIGNED) store_scales((ks >> 2) + 1);
 #pragma unroll
@@ -623,87 +663,123 @@ __device__ __forceinline__ void tile_body(const Mxfp4GemmArgs& a, long long expe
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     }
+    if constexpr (LAST && PHASE == 3) buffer = (buffer + groups) & 1;
 #pragma unroll
     for (int j = 0; j < MM; ++j) {
       constexpr int per = (RD + MM - 1) / MM;
 #pragma unroll
-      for (int p = j * per; p < (j + 1) * per && p < RD; ++p) read_piece(ks + 1, 0, p, f0, true);
+      for (int p = j * per; p < (j + 1) * per && p < RD; ++p) {
+        if constexpr (LAST && PHASE == 3) read_piece(0, 0, p, f0, true);   // buffer: the next tile's by now
+        else read_piece(ks + 1, 0, p, f0, true);
+      }
       if constexpr (PHASE & 1) {
 #pragma unroll
-        for (int i = j * S::LPP / MM; i < (j + 1) * S::LPP / MM; ++i) issue((ks >> 1) + 2, i);
+        for (int i = j * S::LPP / MM; i < (j + 1) * S::LPP / MM; ++i) issue(LAST ? PHASE >> 1 : (ks >> 1) + 2, i);
       }
       __builtin_amdgcn_sched_barrier(0);
       acc[j / NT][j % NT] = mma32<1>(f1.w[j % NT], ws4[j % NT], f1.x[j / NT], xs[j / NT], acc[j / NT][j % NT]);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  for (int ks = 0; ks < steps; ks += 4) {        // whole groups of four: steps past K add nothing
-    step(ks, std::integral_constant<int, 0>{});
-    step(ks + 1, std::integral_constant<int, 1>{});
-    step(ks + 2, std::integral_constant<int, 2>{});
-    step(ks + 3, std::integral_constant<int, 3>{});
-  }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the copies past the end land before LDS is given up
-
-  if constexpr (MODE == kFc1) {
-    const int col = cg * (S::TC / 2) + 32 * wc;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int i = 32 * (wt * MT + m) + r32;
-      const long long row = row0 + i;
-      store_swiglu32(acc[m][0], acc[m][1], a.bq + row * (inter / 2) + col / 2, a.bs + row * (inter / 32) + col / 32, h,
-                     i < nrows && col < inter);
-    }
-  } else {
-    // Rows of y are written whole: 32 rows at a time pass through the wavefront's own part of the ring (rows
-    // padded by 16 bytes), so that a store covers 256 or 512 neighbouring bytes of a row (8- or 16-byte
-    // pieces straight from the registers: 22 us of the 52.9 at T = 4096, K = N = 4096).
-    constexpr bool BF = MODE == kDenseBf16;
-    constexpr int ES = BF ? 2 : 4, EPL = 16 / ES, PITCH = 32 * NT * ES + 16;
-    static_assert(4 * 32 * PITCH <= S::kLds, "four wavefronts' rows fit the ring");
-    const int col0 = cg * S::TC + 32 * NT * wc;
-    if (a.N % EPL == 0) {
-      __syncthreads();                           // every wavefront has read its last fragments
-      uint8_t* mine = lds + wv * 32 * PITCH;
+  auto store_tile = [&](const TileAt& t) {
+    if constexpr (MODE == kFc1) {
+      const int col = t.cg * (S::TC / 2) + 32 * wc;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
+        const int i = 32 * (wt * MT + m) + r32;
+        const long long row = t.row0 + i;
+        if constexpr (STREAM) __builtin_amdgcn_sched_barrier(0);
+        store_swiglu32(acc[m][0], acc[m][1], a.bq + row * (inter / 2) + col / 2, a.bs + row * (inter / 32) + col / 32, h,
+                       i < t.nrows && col < inter);
+      }
+    } else {
+      // Rows of y are written whole: 32 rows at a time pass through the wavefront's own part of the ring (rows
+      // padded by 16 bytes), so that a store covers 256 or 512 neighbouring bytes of a row (8- or 16-byte
+      // pieces straight from the registers: 22 us of the 52.9 at T = 4096, K = N = 4096).
+      constexpr bool BF = MODE == kDenseBf16;
+      constexpr int ES = BF ? 2 : 4, EPL = 16 / ES, PITCH = 32 * NT * ES + 16;
+      static_assert(4 * 32 * PITCH <= S::kLds, "four wavefronts' rows fit the ring");
+      const int col0 = t.cg * S::TC + 32 * NT * wc;
+      if (a.N % EPL == 0) {
+        __syncthreads();                           // every wavefront has read its last fragments
+        uint8_t* mine = lds + wv * 32 * PITCH;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f4 v = {acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
+              uint8_t* to = mine + r32 * PITCH + (32 * n + 8 * q + 4 * h) * ES;
+              if constexpr (BF) *reinterpret_cast<bf4*>(to) = __builtin_convertvector(v, bf4);
+              else *reinterpret_cast<f4*>(to) = v;
+            }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          constexpr int LPR = 32 * NT / EPL, RPI = 64 / LPR;     // lanes a row, rows a store
+          const int c = col0 + (lane % LPR) * EPL;
+#pragma unroll
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int r = RPI * i + lane / LPR, row = 32 * (wt * MT + m) + r;
+            const i4v v = *reinterpret_cast<const i4v*>(mine + r * PITCH + (lane % LPR) * 16);
+            if (row < t.nrows && c < a.N)
+              *reinterpret_cast<i4v*>(static_cast<uint8_t*>(a.y) + (static_cast<long long>(t.row0 + row) * a.N + c) * ES) = v;
+          }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+        return;
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int i = 32 * (wt * MT + m) + r32;
+        const long long row = static_cast<long long>(t.row0 + i) * a.N;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
+            const int col = col0 + 32 * n + 8 * q + 4 * h;
             const f4 v = {acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
-            uint8_t* to = mine + r32 * PITCH + (32 * n + 8 * q + 4 * h) * ES;
-            if constexpr (BF) *reinterpret_cast<bf4*>(to) = __builtin_convertvector(v, bf4);
-            else *reinterpret_cast<f4*>(to) = v;
+            if (i < t.nrows) store4<BF, false>(a.y, row + col, col, a.N, v);
           }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        constexpr int LPR = 32 * NT / EPL, RPI = 64 / LPR;     // lanes a row, rows a store
-        const int c = col0 + (lane % LPR) * EPL;
-#pragma unroll
-        for (int i = 0; i < 32 / RPI; ++i) {
-          const int r = RPI * i + lane / LPR, row = 32 * (wt * MT + m) + r;
-          const i4v v = *reinterpret_cast<const i4v*>(mine + r * PITCH + (lane % LPR) * 16);
-          if (row < nrows && c < a.N)
-            *reinterpret_cast<i4v*>(static_cast<uint8_t*>(a.y) + (static_cast<long long>(row0 + row) * a.N + c) * ES) = v;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
-      return;
     }
+  };
+  auto four = [&](int ks, auto last) {
+    step(ks, std::integral_constant<int, 0>{}, last);
+    step(ks + 1, std::integral_constant<int, 1>{}, last);
+    step(ks + 2, std::integral_constant<int, 2>{}, last);
+    step(ks + 3, std::integral_constant<int, 3>{}, last);
+  };
+  for (;;) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int i = 32 * (wt * MT + m) + r32;
-      const long long row = static_cast<long long>(row0 + i) * a.N;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) acc[m][n] = f16v{};
+    bool more = false;
+    if constexpr (STREAM) {
+      TileAt then = t;
+      more = next(then);                         // without a next tile the copies repeat this one's
+      read_routes(then);                         // used a group later
+      __builtin_amdgcn_sched_barrier(0);
+      int g = 0;                                 // K is more than 512: at least two groups
+      do four(4 * g, std::false_type{});
+      while (++g + 1 < groups);
+      point_at(then);
+      four(4 * g, std::true_type{});
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = col0 + 32 * n + 8 * q + 4 * h;
-          const f4 v = {acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
-          if (i < nrows) store4<BF, false>(a.y, row + col, col, a.N, v);
-        }
+      for (int m = 0; m < MT; ++m)               // opaque: else products sink into the branches of the stores
+#pragma unroll
+        for (int n = 0; n < NT; ++n) asm volatile("" : "+v"(acc[m][n]));
+      store_tile(t);
+      __builtin_amdgcn_sched_barrier(0);
+      t = then;
+    } else {
+      for (int g = 0; g < groups; ++g) four(4 * g, std::false_type{});
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the copies past the end land before LDS is given up
+      store_tile(t);
     }
+    if (!more) break;
   }
+  if constexpr (STREAM) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 // Dense: row tiles by column tiles in groups of eight row tiles, a contiguous run of them to each of the
@@ -720,7 +796,7 @@ __global__ __launch_bounds__(256, MT * NT > 8 ? 1 : 2) void k_mxfp4_tile_dense(M
   const int rows_g = min(G, row_tiles - g * G);
   const int rt = g * G + in % rows_g, ct = in / rows_g;
   const int row0 = rt * S::TR;
-  tile_body<MODE, WT, WC, MT, NT, ALIGNED>(a, 0, row0, min(S::TR, a.rows - row0), ct, lds);
+  tile_body<MODE, WT, WC, MT, NT, ALIGNED>(a, TileAt{0, row0, min(S::TR, a.rows - row0), ct}, NoNext{}, lds);
 }
 
 // Grouped: tiles of up to 128 rows of one expert by 256 columns (first product: 128 gate and 128 up). A tile's
@@ -735,8 +811,37 @@ __global__ __launch_bounds__(256, 2) void k_mxfp4_tile_grouped(Mxfp4GemmArgs a, 
   const int4 t = a.gtiles[min(tile, a.max_gtiles - 1)];      // read beside the count, not after it
   if (tile >= *a.num_gtiles) return;
   const long long expert = t.x & 0xffffff;
-  if (t.z > 64) tile_body<MODE, 2, 2, 2, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
-  else tile_body<MODE, 2, 2, 1, 2, ALIGNED>(a, expert, t.y, t.z, ct, lds);
+  if (t.z > 64) tile_body<MODE, 2, 2, 2, 2, ALIGNED>(a, TileAt{expert, t.y, t.z, ct}, NoNext{}, lds);
+  else tile_body<MODE, 2, 2, 1, 2, ALIGNED>(a, TileAt{expert, t.y, t.z, ct}, NoNext{}, lds);
+}
+
+// First product, K > 512, more tiles than run at once: the same tiles by a fixed number of workgroups, two a CU, each
+// of which walks over its XCD's tiles without stopping the ring (H = 1024, I = 512, E = 96, k = 8: T = 2048 the layer
+// 82.3 -> 77.7 us, T = 8192 this product 94.9 -> 74.9, T = 700 18.0 -> 17.2; with 384 tiles, one each, 13.7 -> 15.6).
+// The second product's results need the ring's LDS on their way out; with 8 KB of their own instead the layer took 80.6.
+constexpr unsigned kStreamGroups = 512;
+
+__global__ __launch_bounds__(256, 2) void k_mxfp4_tile_stream(Mxfp4GemmArgs a, int col_tiles) {
+  using S = Tile<kFc1, 2, 2, 2, 2>;
+  __shared__ __align__(16) uint8_t lds[S::kLds];
+  const int count = *a.num_gtiles, xcd = blockIdx.x % 8;
+  const int items = count > xcd ? (count - xcd + 7) / 8 * col_tiles : 0;
+  int at = blockIdx.x / 8;
+  if (at >= items) return;
+  auto tile = [&](int at) {
+    // below the count: at < items. Constant address space (the list is of an earlier launch): a scalar load, which
+    // waits for no copy in flight.
+    const i4v t = reinterpret_cast<const __attribute__((address_space(4))) i4v*>(
+        reinterpret_cast<uintptr_t>(a.gtiles))[at / col_tiles * 8 + xcd];
+    return TileAt{t[0] & 0xffffff, t[1], t[2], at % col_tiles};
+  };
+  auto next = [&](TileAt& t) {
+    at += gridDim.x / 8;
+    if (at >= items) return false;
+    t = tile(at);
+    return true;
+  };
+  tile_body<kFc1, 2, 2, 2, 2, true>(a, tile(at), next, lds);
 }
 
 // y_t = sum over j ascending of w[t][j] * v[slot of (t, j)], four columns a thread; eight rows' loads in
@@ -860,6 +965,10 @@ void launch_grouped(const Mxfp4GemmArgs& a, int tile_rows, hipStream_t s) {
   if (tile_rows == 16) return launch_few_rows<MODE>(a, a.max_gtiles, s);
   const int ct = (a.N + 127) / 128;
   const dim3 g((a.max_gtiles + 7) / 8 * 8 * ct);
+  if (MODE == kFc1 && a.K > 512 && g.x > kStreamGroups && scales_aligned(a)) {
+    hipLaunchKernelGGL(k_mxfp4_tile_stream, dim3(kStreamGroups), dim3(256), 0, s, a, ct);
+    return;
+  }
   if (scales_aligned(a)) hipLaunchKernelGGL((k_mxfp4_tile_grouped<MODE, true>), g, dim3(256), 0, s, a, ct);
   else hipLaunchKernelGGL((k_mxfp4_tile_grouped<MODE, false>), g, dim3(256), 0, s, a, ct);
 }
