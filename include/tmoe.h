@@ -263,8 +263,8 @@ tmoe_status tmoe_router_topk(const tmoe_router_config *cfg, const void *logits, 
                              const uint8_t *token_mask, int32_t T, void *ids, float *w, float *lse,
                              void *stream);
 
-/* Balance loss. n = rows with lse > -inf, c_e = ids equal to e, f_e = c_e / sum c, P_e = the mean of
- * exp(l_te - lse_t) over those n rows:
+/* Balance loss. n = rows with lse > -inf (a NaN is not), c_e = ids equal to e (of all rows), f_e = c_e / sum c,
+ * P_e = the mean of exp(l_te - lse_t) over those n rows:
  *   loss = coefficient * E * sum_e f_e P_e          (coefficient for a uniform router; 0 if n = 0)
  * counts: int32 [E], c_e; slope: fp32 [E], dloss/dp_te = coefficient * E * f_e / n (f taken as a
  * constant), which tmoe_router_backward reads. ids and lse as tmoe_router_topk writes them (ids outside
@@ -280,7 +280,7 @@ tmoe_status tmoe_balance_loss(const tmoe_router_config *cfg, const void *logits,
  *   from the weights (w and dw, fp32 [T][k], both given): renormalize = 1
  *       dl_e = w_j (dw_j - sum_i w_i dw_i) where e = ids_j, 0 elsewhere;
  *     renormalize = 0  dl_e = [e = ids_j] w_j dw_j - p_e sum_i w_i dw_i;
- *   from the balance loss (slope and dloss, fp32 [E] and [1], both given):
+ *   from the balance loss (slope and dloss, fp32 [E] and [1], both given), in rows with lse > -inf:
  *       dl_e = dloss p_e (slope_e - sum p slope).
  * Either pair may be null; with both the parts add up in fp32 before the one rounding. Rows with
  * lse = -inf and routes with an id outside [0, E) get nothing, whatever w, dw and the logits hold there.

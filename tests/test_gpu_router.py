@@ -207,6 +207,46 @@ def test_nan_and_infinity_in_a_row_that_counts():
     assert torch.isfinite(d).all() and torch.all(d[:2] == 0)
 
 
+@pytest.mark.parametrize("T,E,k", [(6, 10, 2), (300, 65, 3), (2051, 256, 8)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_balance_loss_leaves_out_rows_whose_lse_is_nan(T, E, k, dtype):
+    """Rows with a NaN or +inf logit that no mask takes out: lse is NaN, which is not > -inf. They add nothing to n and
+    P and get no gradient; their ids are counted like all others. Tolerances as for the healthy batch."""
+    from trellis_quantized_moe_tmoe_amd import router
+    say(f"[case] balance with NaN rows T={T} E={E} k={k} {dtype}")
+    l, _ = _logits(T, E, dtype, 13 * T + E)
+    l[1, E // 2], l[3, E - 1], l[4] = float("nan"), float("inf"), -float("inf")
+    l[5::97, 0] = float("nan")
+    l64, gl = _np(l), l.cuda()
+    ids, w, lse = router.topk(gl, k)
+    bad = np.isnan(l64).any(1) | np.isposinf(l64).any(1)
+    assert np.array_equal(torch.isnan(lse).cpu().numpy(), bad)
+    valid = ~bad & (l64 > -np.inf).any(1)
+    assert valid.any() and not valid[4]
+    healthy = np.where(valid[:, None], l64, 0.0)
+    loss, counts, slope = router.balance_loss(gl, lse, ids, 0.5)
+    want, c, want_slope, p = R.balance(healthy, valid, ids.cpu().numpy(), 0.5)
+    assert c.sum() == (ids >= 0).sum() and np.array_equal(counts.cpu().numpy(), c)
+    assert np.all(np.abs(_np(slope) - want_slope) <= 2 * U * np.abs(want_slope))
+    tol = (2 * _spread(healthy) + 20) * U
+    assert abs(float(loss) - want) <= (tol + (T // 2048 + 8) * U + 4 * U) * abs(want)
+
+    scale = np.float32(0.75 * T * E)
+    dloss = torch.tensor(scale, device="cuda")
+    d = router.backward(gl, lse, ids, slope=slope, dloss=dloss)
+    g = R.balance_grad(p, want_slope, float(scale))
+    bound = float(scale) * p * (want_slope + (p * want_slope).sum(1, keepdims=True)) * (2 * tol + 24 * U)
+    assert np.all(np.abs(_np(d) - g) <= bound + HALF[dtype] * np.abs(g) + TINY[dtype])
+    assert not d[torch.from_numpy(~valid).cuda()].any()
+    # beside the weights' gradient, which is NaN where such a row's weights are: the selected logits, or all of them
+    both = router.backward(gl, lse, ids, w=w, dw=torch.ones_like(w), slope=slope, dloss=dloss)
+    alone = router.backward(gl, lse, ids, w=w, dw=torch.ones_like(w))
+    assert torch.equal(torch.isnan(both), torch.isnan(alone)) and torch.isnan(both).any(1).cpu().numpy().sum() == bad.sum()
+    soft = router.backward(gl, lse, ids, w=w, dw=torch.ones_like(w), renormalize=False, slope=slope, dloss=dloss)
+    assert np.array_equal(torch.isnan(soft).all(1).cpu().numpy(), bad)
+    assert np.array_equal(torch.isnan(soft).any(1).cpu().numpy(), bad)
+
+
 def test_strided_rows_and_large_logits():
     from trellis_quantized_moe_tmoe_amd import router
     wide = torch.full((6, 100), float("nan"), device="cuda")

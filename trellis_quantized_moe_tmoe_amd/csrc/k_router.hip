@@ -215,7 +215,7 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_rows(BalanceArgs
     }
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
-      const bool in = lse[q] != kNegInf;
+      const bool in = lse[q] > kNegInf;          // not so for a NaN: one bad row leaves the others' loss as it is
 #pragma unroll
       for (int j = 0; j < V; ++j) v[q][j] = in ? v[q][j] : kNegInf;
       float inv = row_softmax<V>(v[q], in ? lse[q] : 0.0f);
@@ -328,7 +328,8 @@ __global__ __launch_bounds__(256) void k_balance_finish(BalanceArgs a) {
 
 // Gradient of one row. Top-k part: renormalised weights w_j over the selected logits give
 // w_j (dw_j - sum_i w_i dw_i) at the selected ones (the logits are not read); softmax weights give that
-// sum's share of every expert. Balance part: dloss * p_e (slope_e - sum p slope).
+// sum's share of every expert. Balance part: dloss * p_e (slope_e - sum p slope), for rows with lse > -inf. A row whose
+// lse is NaN (a NaN or +inf logit) has no balance part; its weights are NaN, and the top-k part carries that on.
 // Every load of the row is issued before the first wait; a row with lse = -inf is read and not used.
 template <class D, int V>
 __global__ __launch_bounds__(64 * kWavesPerGroup) void k_router_grad(RouterGradArgs a) {
@@ -360,7 +361,7 @@ __global__ __launch_bounds__(64 * kWavesPerGroup) void k_router_grad(RouterGradA
     dw = a.dw[at];
   }
   const bool in = lse != kNegInf;
-  const bool soft = in && read;
+  const bool soft = lse > kNegInf ? read : in && a.dw != nullptr && !a.renormalize;
   float* mine = at_expert[wv];
   float dot = 0.0f;
   if (a.dw) {

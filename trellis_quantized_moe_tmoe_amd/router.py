@@ -191,7 +191,8 @@ def topk(logits: torch.Tensor, top_k: int, *, renormalize: bool = True, token_ma
 
 def balance_loss(logits: torch.Tensor, lse: torch.Tensor, ids: torch.Tensor, coefficient: float = 1.0):
     """(loss [], counts int32 [E], slope fp32 [E]): coefficient * E * sum_e f_e P_e with the routes' shares f and
-    the mean probabilities P over the rows with lse > -inf; counts per expert; slope = dloss/dp for `backward`."""
+    the mean probabilities P over the rows with lse > -inf; counts per expert; slope = dloss/dp for `backward`.
+    A row whose lse is NaN (a NaN or +inf logit) is left out like one whose lse is -inf; its ids are counted."""
     if _tracked(logits):
         return _BalanceLoss.apply(logits, lse, ids, coefficient)
     return _balance_loss(logits, lse, ids, coefficient)
