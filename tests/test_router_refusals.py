@@ -120,6 +120,27 @@ def test_reference_by_hand():
     assert c.tolist() == [2] * 8 and np.isclose(loss, 0.25)
 
 
+def test_forward_mode_derivatives_are_refused():
+    """A dual tensor has requires_grad False: its tangent must not get lost without a word, without gradients either."""
+    from torch.autograd import forward_ad
+    from trellis_quantized_moe_tmoe_amd import router
+    l, lse, ids = torch.zeros(4, 16), torch.zeros(4), torch.zeros(4, 2, dtype=torch.int64)
+    w, slope, one = torch.zeros(4, 2), torch.zeros(16), torch.ones(())
+    with forward_ad.dual_level(), torch.no_grad():
+        d = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        assert not d(l).requires_grad
+        for bad in [lambda: router.topk(d(l), 2), lambda: router.balance_loss(d(l), lse, ids),
+                    lambda: router.balance_loss(l, d(lse), ids), lambda: router.backward(d(l), lse, ids, w=w, dw=w),
+                    lambda: router.backward(l, d(lse), ids, w=w, dw=w), lambda: router.backward(l, lse, ids, w=d(w), dw=w),
+                    lambda: router.backward(l, lse, ids, w=w, dw=d(w)),
+                    lambda: router.backward(l, lse, ids, slope=d(slope), dloss=one),
+                    lambda: router.backward(l, lse, ids, slope=slope, dloss=d(one))]:
+            with pytest.raises(ValueError, match="forward-mode"):
+                bad()
+        with pytest.raises(ValueError, match="GPU device"):      # beside a dual, other tensors go on as they did
+            router.topk(l, 2)
+
+
 def test_sizes_past_32_bits():
     """2^32 + 5 rows or experts must not pass for 5."""
     from trellis_quantized_moe_tmoe_amd import router

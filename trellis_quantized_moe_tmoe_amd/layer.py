@@ -9,6 +9,7 @@ from typing import Optional
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad
 
 from . import native
 from .native import check, lib
@@ -74,6 +75,17 @@ def _one_gpu(first, *others) -> bool:
         if t.get_device() != index:
             return False
     return True
+
+
+def _refuse_duals(**tensors) -> None:
+    """Raise ValueError for a tensor with a forward-mode tangent: kernels read addresses, so it would get lost."""
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{name}: forward-mode derivatives are not available")
+
+
+def _in_forward_mode() -> bool:
+    return getattr(forward_ad, "_current_level", 0) >= 0
 
 
 def _launch(index: int, fn, where: str, *args) -> None:

@@ -4,7 +4,9 @@ Thin wrappers of tmoe_router_topk, tmoe_balance_loss and tmoe_router_backward (i
 formulas). `topk` gives the ids and weights that `layer.Plan.forward` takes; rows left out and experts
 that are not available come out as id -1, which the layer drops.
 
-`topk` and `balance_loss` record a gradient where the logits require one (first derivatives only).
+`topk` and `balance_loss` record a gradient where the logits require one (first derivatives only; tensors with a
+forward-mode tangent are refused). It flows from `w` and `loss`; `lse`, `counts` and `slope` are not differentiable, so
+a loss computed from them trains nothing.
 `backward` is the same gradient as one explicit call, for programs without autograd and for hipGraph
 capture."""
 from __future__ import annotations
@@ -16,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import native
-from .layer import _fits, _int32, _launch, _one_gpu, _require, _same_device
+from .layer import _fits, _in_forward_mode, _int32, _launch, _one_gpu, _refuse_duals, _require, _same_device
 from .native import check, lib
 
 _DTYPES = {torch.float32: native.F32, torch.bfloat16: native.BF16, torch.float16: native.F16}
@@ -108,6 +110,8 @@ def backward(logits: torch.Tensor, lse: torch.Tensor, ids: torch.Tensor, *, w: O
              dloss: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of the logits [T, E], in their type, from the weights' gradient (w and dw [T, k]) and/or the
     balance loss's (slope [E] as `balance_loss` returns it, and dloss, one value on the GPU)."""
+    if _in_forward_mode():
+        _refuse_duals(logits=logits, lse=lse, w=w, dw=dw, slope=slope, dloss=dloss)
     T = _tokens(logits)
     k = _check_ids(ids, T)
     cfg, stride = _config(logits, k, ids.dtype, renormalize)
@@ -184,6 +188,8 @@ def topk(logits: torch.Tensor, top_k: int, *, renormalize: bool = True, token_ma
 
     renormalize: weights are a softmax over the k selected logits, else the whole row's softmax at them.
     token_mask [T] (bool or uint8): rows that are 0 get ids -1, weights 0 and lse -inf."""
+    if _in_forward_mode():
+        _refuse_duals(logits=logits)
     if _tracked(logits):
         return _TopK.apply(logits, top_k, renormalize, token_mask, ids_dtype)
     return _topk(logits, top_k, renormalize, token_mask, ids_dtype)
@@ -193,6 +199,8 @@ def balance_loss(logits: torch.Tensor, lse: torch.Tensor, ids: torch.Tensor, coe
     """(loss [], counts int32 [E], slope fp32 [E]): coefficient * E * sum_e f_e P_e with the routes' shares f and
     the mean probabilities P over the rows with lse > -inf; counts per expert; slope = dloss/dp for `backward`.
     A row whose lse is NaN (a NaN or +inf logit) is left out like one whose lse is -inf; its ids are counted."""
+    if _in_forward_mode():
+        _refuse_duals(logits=logits, lse=lse)
     if _tracked(logits):
         return _BalanceLoss.apply(logits, lse, ids, coefficient)
     return _balance_loss(logits, lse, ids, coefficient)
