@@ -316,7 +316,8 @@ tmoe_status tmoe_linear_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, i
 
 /* The routed expert layer with MXFP4 weights and activations (q = the rounding above):
  *   [G | U] = W1_e q(x_t);  b = q(silu(G) * U);  y_t = sum over j ascending of w[t][j] * (W2_e b)
- * for e = ids[t][j]; ids outside [0, E) are dropped routes. No rotations, signs or channel scales. */
+ * for e = ids[t][j]; ids outside [0, E) are dropped routes. No rotations, signs or channel scales. Forward only:
+ * the rows W2_e b, from which a gradient of w would follow, stay in the scratch. */
 typedef struct {
   int32_t hidden;              /* H: multiple of 32, 32..8192                                   */
   int32_t inter;               /* I: multiple of 32, 32..8192                                   */

@@ -369,3 +369,23 @@ def test_router_quantisation_and_layer_together():
     assert torch.all(y[~mask.cuda()] == 0) and torch.isfinite(loss)
     d = router.backward(logits, lse, ids, w=w, dw=torch.ones_like(w), slope=slope, dloss=torch.ones((), device="cuda"))
     assert torch.isfinite(d).all() and torch.all(d[~mask.cuda()] == 0)
+
+
+def test_weights_of_a_tracked_router():
+    """topk's weights carry a gradient that the layer cannot pass on: refused; the same call without gradients runs."""
+    from trellis_quantized_moe_tmoe_amd import router
+    mx = _mx()
+    T, H, I, E, k = 5, 64, 32, 4, 2
+    g = torch.Generator().manual_seed(3)
+    weights = mx.ExpertWeights(*mx.quantize(torch.randn(E, 2 * I, H, generator=g).cuda()),
+                               *mx.quantize(torch.randn(E, H, I, generator=g).cuda()))
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    logits = torch.randn(T, E, generator=g).cuda().requires_grad_()
+    plan = mx.ExpertPlan(H, I, E, k, T)
+    scratch = plan.alloc_scratch()
+    ids, w, lse = router.topk(logits, k)
+    with pytest.raises(ValueError, match="w: requires a gradient"):
+        plan.forward(x, ids, w, weights, scratch)
+    y = plan.forward(x, ids, w.detach(), weights, scratch)
+    with torch.no_grad():
+        assert torch.equal(plan.forward(x, ids, w, weights, scratch), y)

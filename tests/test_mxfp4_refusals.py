@@ -116,6 +116,34 @@ def test_binding_refuses_what_does_not_fit():
             bad()
 
 
+def test_gradients_are_refused_not_lost():
+    """The calls read addresses and have no backward: a tensor that wants a gradient, in either mode, is refused unless
+    gradients are off; the bf16 activations and the router's weights of a training step among them."""
+    from torch.autograd import forward_ad
+    from trellis_quantized_moe_tmoe_amd import mxfp4
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    plan = mxfp4.ExpertPlan(64, 32, 4, 2, 8)
+    a = dict(x=torch.zeros(3, 64, dtype=torch.bfloat16), ids=torch.zeros(3, 2, dtype=torch.int64), w=torch.zeros(3, 2),
+             weights=mxfp4.ExpertWeights(u8(4, 64, 32), u8(4, 64, 2), u8(4, 64, 16), u8(4, 64, 1)),
+             scratch=u8(plan.scratch_bytes), y=torch.zeros(3, 64))
+    logits = torch.zeros(3, 4, requires_grad=True)
+    calls = [lambda f: mxfp4.quantize(f(torch.zeros(4, 64)) * 1.0),    # an activation: something lies behind it
+             lambda f: mxfp4.linear(u8(4, 32), u8(4, 2), u8(6, 32), u8(6, 2), y=f(torch.zeros(4, 6)))]
+    calls += [lambda f, n=n: plan.forward(**{**a, n: f(a[n])}) for n in ("x", "w", "y")]
+    leaf = lambda t: t.clone().requires_grad_()  # noqa: E731
+    for call in calls:
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call(leaf)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU device"):
+            call(leaf)
+        with forward_ad.dual_level(), torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):
+            call(lambda t: forward_ad.make_dual(t, torch.ones_like(t)))
+    with pytest.raises(ValueError, match="GPU device"):                # a parameter, as a program loads it
+        mxfp4.quantize(torch.nn.Parameter(torch.zeros(4, 64)))
+    with pytest.raises(ValueError, match="w: requires a gradient"):
+        plan.forward(**{**a, "w": torch.softmax(logits, 1)[:, :2].contiguous()})
+
+
 def test_reference_by_hand():
     x = np.zeros(64)
     x[:8] = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]

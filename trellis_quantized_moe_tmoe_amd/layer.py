@@ -88,6 +88,17 @@ def _in_forward_mode() -> bool:
     return getattr(forward_ad, "_current_level", 0) >= 0
 
 
+def _no_gradient(**tensors) -> None:
+    """Raise ValueError for a tensor that wants a gradient, where the call has none to give."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{name}: requires a gradient, which this call does not give; detach it or call under "
+                                 "torch.no_grad()")
+    if _in_forward_mode():
+        _refuse_duals(**tensors)
+
+
 def _launch(index: int, fn, where: str, *args) -> None:
     """fn(*args, stream) with GPU `index` current and its current torch stream, raising on an error status."""
     if index == _current_device():

@@ -3,7 +3,10 @@
 Thin wrappers of tmoe_mxfp4_quantize, tmoe_mxfp4_dequantize, tmoe_linear_mxfp4 and tmoe_forward_mxfp4
 (include/tmoe.h holds the format and the formulas). Codes and scales are uint8 tensors [..., K/2] and
 [..., K/32]; weights are rows of output features, quantised along their input features:
-`ExpertWeights(*quantize(w1), *quantize(w2))` with w1 [E, 2I, H] (gate rows first) and w2 [E, H, I]."""
+`ExpertWeights(*quantize(w1), *quantize(w2))` with w1 [E, 2I, H] (gate rows first) and w2 [E, H, I].
+
+Forward only: no call here has a backward. Activations, weights of routes and outputs that require a gradient are
+refused (detach them, or call under torch.no_grad()); a leaf parameter can be quantised as it is."""
 from __future__ import annotations
 
 import ctypes
@@ -12,7 +15,8 @@ from typing import Optional
 import torch
 
 from . import native
-from .layer import _BITS16, _check_scratch, _fits, _int32, _launch, _one_gpu, _require, _same_device
+from .layer import _BITS16, _check_scratch, _fits, _in_forward_mode, _int32, _launch, _no_gradient, _one_gpu, \
+    _refuse_duals, _require, _same_device
 from .native import check, lib
 
 _DTYPES = {torch.float32: native.F32, torch.bfloat16: native.BF16, torch.float16: native.F16}
@@ -29,6 +33,10 @@ def quantize(x: torch.Tensor):
     """(codes uint8 [..., K/2], scales uint8 [..., K/32]) of fp32, bf16 or fp16 values [..., K], K a multiple of 32."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x: expected a tensor [..., K]")
+    if x.grad_fn is not None:                     # a parameter itself may be quantised: nothing lies behind it
+        _no_gradient(x=x)
+    elif _in_forward_mode():
+        _refuse_duals(x=x)
     lead, K = x.shape[:-1], x.shape[-1]
     if x.dtype not in _DTYPES or not x.is_contiguous():
         _require(x, "x", x.shape, tuple(_DTYPES))
@@ -87,8 +95,10 @@ def linear(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
     T, N, out, dev = x_codes.shape[0], w_codes.shape[0], _out_dtype(out_dtype), x_codes.device
     if y is None:
         y = torch.empty((T, N), dtype=out_dtype, device=dev)
-    elif not _fits(y, (T, N), out_dtype):
-        _require(y, "y", (T, N), (out_dtype,))
+    else:
+        _no_gradient(y=y)
+        if not _fits(y, (T, N), out_dtype):
+            _require(y, "y", (T, N), (out_dtype,))
     if not _one_gpu(x_codes, x_scales, w_codes, w_scales, y):
         _same_device([("x codes", x_codes), ("x scales", x_scales), ("w codes", w_codes), ("w scales", w_scales),
                       ("y", y)])
@@ -147,6 +157,7 @@ class ExpertPlan:
     def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, weights: ExpertWeights,
                 scratch: torch.Tensor, y: Optional[torch.Tensor] = None) -> torch.Tensor:
         """y [T, H] of x bf16 [T, H] (or its bit patterns), ids [T, k], w fp32 [T, k]."""
+        _no_gradient(x=x, w=w, y=y)
         T = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else -1
         if y is None and isinstance(x, torch.Tensor):
             y = torch.empty((max(T, 0), self.hidden), dtype=self.out_dtype, device=x.device)
