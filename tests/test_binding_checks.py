@@ -2,6 +2,8 @@
 (which sees raw pointers only and cannot check buffer sizes). Every case here must raise ValueError
 before any launch; the tensors live on the CPU, so a call that slipped through would be caught by
 the final device check rather than reaching a kernel."""
+import warnings
+
 import numpy as np
 import pytest
 import torch
@@ -55,6 +57,26 @@ def test_layer_rejects_mismatched_tensors(field, bad, msg):
     for stages in (False, True):
         with pytest.raises(ValueError, match=msg):
             _call(plan, weights, a, stages)
+
+
+def test_layer_warns_where_a_gradient_ends():
+    """The layer is forward only: weights that carry a gradient (as router.topk gives them for tracked logits) run as
+    ever, but not without a word."""
+    _, plan, weights, a = _cpu_case()
+    for stages in (False, True):
+        for name in ("w", "x"):
+            b = dict(a)
+            b[name] = (a[name] if name == "w" else a[name].view(torch.bfloat16)).clone().requires_grad_()
+            with pytest.raises(ValueError, match="GPU device"), pytest.warns(UserWarning, match=f"{name} requires a grad"):
+                _call(plan, weights, b, stages)
+            with torch.no_grad(), warnings.catch_warnings():
+                warnings.simplefilter("error")
+                with pytest.raises(ValueError, match="GPU device"):
+                    _call(plan, weights, b, stages)
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            with pytest.raises(ValueError, match="GPU device"):
+                _call(plan, weights, a, stages)
 
 
 def test_layer_rejects_int32_ids_on_an_int64_plan_and_back():

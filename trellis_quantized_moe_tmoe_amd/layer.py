@@ -5,6 +5,7 @@ pointers, sizes and the current stream."""
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import Optional
 
 import numpy as np
@@ -246,7 +247,8 @@ class Plan:
     def check_call(self, x, ids, w, weights, scratch, y) -> None:
         """Raise ValueError unless the tensors match what the forward reads and writes: x bf16 bits
         [T, H]; ids [T, k] of the plan's id dtype; w fp32 [T, k]; y fp32 [T, H]; weights of this
-        plan's shapes; scratch at least the planned bytes; all contiguous, on one GPU device."""
+        plan's shapes; scratch at least the planned bytes; all contiguous, on one GPU device. Warns
+        where x or w requires a gradient, which ends here."""
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             raise ValueError("x: expected a 2-D tensor [T, H]")
         T = x.shape[0]
@@ -256,6 +258,9 @@ class Plan:
         _require(x, "x", (T, H), _BITS16)
         _require(ids, "ids", (T, k), (self.ids_dtype,))
         _require(w, "w", (T, k), (torch.float32,))
+        if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+            warnings.warn(f"{'w' if w.requires_grad else 'x'} requires a gradient: the layer is forward only and none "
+                          "flows back through it", stacklevel=3)
         _require(y, "y", (T, H), (torch.float32,))
         if not isinstance(weights, DeviceWeights):
             raise ValueError("weights: expected DeviceWeights")
