@@ -120,6 +120,23 @@ def test_reference_by_hand():
     assert c.tolist() == [2] * 8 and np.isclose(loss, 0.25)
 
 
+def test_configurations_are_refused_before_the_outputs_are_allocated(monkeypatch):
+    """A top_k that no configuration allows must come back as the library's refusal, not as what the allocator says of
+    outputs [T, top_k]: negative sizes, or more memory than there is."""
+    from trellis_quantized_moe_tmoe_amd import native, router
+    l, made = torch.zeros(4, 16), []
+    monkeypatch.setattr(router, "_one_gpu", lambda *t: True)         # as if on a GPU: no call below gets as far
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(a) or pytest.fail("allocated"))
+    mask = torch.ones(4, dtype=torch.bool)
+    for top_k, name in [(-1, "INVALID_ARG"), (0, "INVALID_ARG"), (17, "INVALID_ARG"), (33, "UNSUPPORTED"),
+                        (2 ** 30, "UNSUPPORTED"), (-2 ** 30, "INVALID_ARG")]:
+        with pytest.raises(native.TmoeError, match=name):
+            router.topk(l, top_k, token_mask=mask)
+    with pytest.raises(native.TmoeError, match="UNSUPPORTED"):
+        router.topk(torch.zeros(2, 513), 2, token_mask=mask[:2])
+    assert not made
+
+
 def test_forward_mode_derivatives_are_refused():
     """A dual tensor has requires_grad False: its tangent must not get lost without a word, without gradients either."""
     from torch.autograd import forward_ad

@@ -27,8 +27,11 @@ _IDS = {torch.int32: native.IDS_I32, torch.int64: native.IDS_I64}
 
 @functools.lru_cache(maxsize=256)
 def _packed(E: int, top_k: int, dtype, ids_dtype, renormalize: bool):
-    cfg = native.RouterConfig(E, top_k, _DTYPES[dtype], _IDS[ids_dtype], int(renormalize))
-    return ctypes.byref(cfg)                      # keeps cfg alive
+    cfg = ctypes.byref(native.RouterConfig(E, top_k, _DTYPES[dtype], _IDS[ids_dtype], int(renormalize)))   # kept alive
+    need = ctypes.c_size_t()
+    # refused here, before a wrapper allocates outputs of these sizes
+    check(lib.tmoe_balance_loss_scratch(cfg, 0, ctypes.byref(need)), "router configuration")
+    return cfg
 
 
 @functools.lru_cache(maxsize=256)
