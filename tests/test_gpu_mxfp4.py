@@ -389,3 +389,30 @@ def test_weights_of_a_tracked_router():
     y = plan.forward(x, ids, w.detach(), weights, scratch)
     with torch.no_grad():
         assert torch.equal(plan.forward(x, ids, w, weights, scratch), y)
+
+
+def test_an_output_that_a_backward_still_needs():
+    """y is written in place: a gradient that saved it before must fail, as after torch's own in-place operations,
+    not be computed from the new values."""
+    mx = _mx()
+    g = torch.Generator().manual_seed(4)
+    xq, xs = mx.quantize(torch.randn(3, 64, generator=g).cuda())
+    wq, ws = mx.quantize(torch.randn(5, 64, generator=g).cuda())
+    plan = mx.ExpertPlan(64, 32, 4, 2, 3)
+    weights = mx.ExpertWeights(*mx.quantize(torch.randn(4, 64, 64, generator=g).cuda()),
+                               *mx.quantize(torch.randn(4, 64, 32, generator=g).cuda()))
+    x = torch.randn(3, 64, generator=g).to(torch.bfloat16).cuda()
+    ids, w, scratch = torch.zeros(3, 2, dtype=torch.int64, device="cuda"), torch.ones(3, 2, device="cuda"), plan.alloc_scratch()
+    for y, call in [(torch.empty(3, 5, device="cuda"), lambda y: mx.linear(xq, xs, wq, ws, y=y)),
+                    (torch.empty(3, 64, device="cuda"), lambda y: plan.forward(x, ids, w, weights, scratch, y=y))]:
+        gate = torch.ones((), device="cuda", requires_grad=True)
+        out = (call(y) * gate).sum()
+        out.backward()
+        assert torch.equal(gate.grad, y.sum())
+        out = (call(y) * gate).sum()
+        call(y)
+        with pytest.raises(RuntimeError, match="inplace"):
+            out.backward()
+        with torch.inference_mode():
+            kept = torch.empty_like(y)
+            assert call(kept) is kept and torch.equal(kept, y)

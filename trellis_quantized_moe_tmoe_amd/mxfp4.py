@@ -13,6 +13,7 @@ import ctypes
 from typing import Optional
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import native
 from .layer import _BITS16, _check_scratch, _fits, _in_forward_mode, _int32, _launch, _no_gradient, _one_gpu, \
@@ -99,6 +100,7 @@ def linear(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
         _no_gradient(y=y)
         if not _fits(y, (T, N), out_dtype):
             _require(y, "y", (T, N), (out_dtype,))
+        increment_version(y)                      # a graph that saved y learns that it is written
     if not _one_gpu(x_codes, x_scales, w_codes, w_scales, y):
         _same_device([("x codes", x_codes), ("x scales", x_scales), ("w codes", w_codes), ("w scales", w_scales),
                       ("y", y)])
@@ -158,6 +160,8 @@ class ExpertPlan:
                 scratch: torch.Tensor, y: Optional[torch.Tensor] = None) -> torch.Tensor:
         """y [T, H] of x bf16 [T, H] (or its bit patterns), ids [T, k], w fp32 [T, k]."""
         _no_gradient(x=x, w=w, y=y)
+        if isinstance(y, torch.Tensor):
+            increment_version(y)                  # a graph that saved y learns that it is written
         T = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else -1
         if y is None and isinstance(x, torch.Tensor):
             y = torch.empty((max(T, 0), self.hidden), dtype=self.out_dtype, device=x.device)
