@@ -103,8 +103,9 @@ __device__ __forceinline__ void store4(void* y, long long at, int col, int N, f4
   }
 }
 
-// x / (1 + exp(-x)) with the hardware's 2^y and reciprocal (one unit in the last place each, and |x| half steps
-// from the exponent's product): a few 2^-24 beside the 2^-4 of the codes that follow.
+// x / (1 + exp(-x)) with the hardware's 2^y and reciprocal: off by one unit in the last place each, and for negative x by
+// up to |x| half steps (2^-24) from the exponent's product, 17 of them at x = -20. The codes that follow are rounded by
+// up to 2^-2 of their value, so this can only move a value that lies on the border of two codes.
 __device__ __forceinline__ float silu(float x) {
   return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }
@@ -799,9 +800,10 @@ __global__ __launch_bounds__(256, MT * NT > 8 ? 1 : 2) void k_mxfp4_tile_dense(M
   tile_body<MODE, WT, WC, MT, NT, ALIGNED>(a, TileAt{0, row0, min(S::TR, a.rows - row0), ct}, NoNext{}, lds);
 }
 
-// Grouped: tiles of up to 128 rows of one expert by 256 columns (first product: 128 gate and 128 up). A tile's
-// column blocks go to one XCD, which then reads its rows once. Tiles of at most 64 rows run with half the
-// row fragments; the tile list holds them last.
+// Grouped: tiles of up to 128 rows of one expert by 128 columns (first product: 64 gate and 64 up). A tile's
+// column blocks go to one XCD, which then reads its rows once; fewer than eight tiles therefore keep as few XCDs busy
+// (E = 1, H = 4096, I = 8192: 31 us for the layer with 10 routes, without a tile list, 67 with 11). Tiles of at most 64
+// rows run with half the row fragments; the tile list holds them last.
 template <int MODE, bool ALIGNED>
 __global__ __launch_bounds__(256, 2) void k_mxfp4_tile_grouped(Mxfp4GemmArgs a, int col_tiles) {
   using S = Tile<MODE, 2, 2, 2, 2>;
@@ -815,10 +817,13 @@ __global__ __launch_bounds__(256, 2) void k_mxfp4_tile_grouped(Mxfp4GemmArgs a, 
   else tile_body<MODE, 2, 2, 1, 2, ALIGNED>(a, TileAt{expert, t.y, t.z, ct}, NoNext{}, lds);
 }
 
-// First product, K > 512, more tiles than run at once: the same tiles by a fixed number of workgroups, two a CU, each
-// of which walks over its XCD's tiles without stopping the ring (H = 1024, I = 512, E = 96, k = 8: T = 2048 the layer
-// 82.3 -> 77.7 us, T = 8192 this product 94.9 -> 74.9, T = 700 18.0 -> 17.2; with 384 tiles, one each, 13.7 -> 15.6).
-// The second product's results need the ring's LDS on their way out; with 8 KB of their own instead the layer took 80.6.
+// First product, K > 512, more workgroups in the grouped launch (room for the largest tile list, in whole eights) than
+// run at once: the same tiles by a fixed number of workgroups, two a CU, each of which walks over its XCD's tiles
+// without stopping the ring (H = 1024, I = 512, E = 96, k = 8: T = 2048 the layer 82.3 -> 77.7 us, T = 8192 this product
+// 94.9 -> 74.9, T = 700 18.0 -> 17.2; with 384 tiles, one each, 13.7 -> 15.6). The layer on other geometries, streaming
+// and one each: H = 2048, I = 768, E = 16, k = 2, T = 2048 (576 workgroups) 55.4 and 54.5, T = 8192 (1728) 146.7 and
+// 149.2; H = 4096, I = 1024, E = 8, k = 2, T = 2048 (640) 96.6 and 95.2, T = 8192 (2176) 322.7 and 325.7. All tiles run
+// with all row fragments here, short ones too. The second product's results need the ring's LDS on their way out; with 8 KB of their own instead the layer took 80.6.
 constexpr unsigned kStreamGroups = 512;
 
 __global__ __launch_bounds__(256, 2) void k_mxfp4_tile_stream(Mxfp4GemmArgs a, int col_tiles) {
@@ -886,7 +891,12 @@ __global__ __launch_bounds__(256) void k_mxfp4_combine(Mxfp4CombineArgs a) {
 }  // namespace
 
 // Rows of a tile of the expert layer: 16 while experts hold a few rows each (straight from global memory; up to
-// kFewRoutesMax routes without a tile list), else 128 (through LDS).
+// kFewRoutesMax routes without a tile list), else 128 (through LDS). The layer with a tile list, 16-row and 128-row
+// tiles (us), at 6, 10, 12, 16 and 24 routes an expert:
+//   H = 1024, I = 512, E = 96, k = 8     32.1 34.6   35.0 35.6   36.6 37.3   40.5 37.3   50.8 40.6
+//   H = 1024, I = 512, E = 256, k = 8    67.3 67.4   74.0 71.3   77.3 72.0   90.2 76.3   110.9 79.3
+//   H = 2560, I = 320, E = 128, k = 10   54.6 69.4   59.7 72.7   61.8 73.0   72.7 75.3   89.8 80.9
+//   H = 2048, I = 768, E = 16, k = 2 (16 and 24)                             27.2 23.8   31.4 24.6
 int mxfp4_tile_rows(long long routes, int experts) {
   if (routes > 10LL * experts) return 128;
   return routes <= kFewRoutesMax ? kFewRoutes : 16;
@@ -913,7 +923,9 @@ void launch_rows(const Mxfp4GemmArgs& a, hipStream_t s) {
 }
 
 // The shape of the dense product, by the number of 128 x 128 tiles (us; K = 4096 unless said):
-//   T <= 64         wavefronts that split K (T = 48, N = 1024: 7.6, 64 x 128 tiles 8.5; K = 2560: 5.1 and 6.4)
+//   T <= 64         wavefronts that split K (T = 48, N = 1024: 7.6, 64 x 128 tiles 8.5; K = 2560: 5.1 and 6.4;
+//                   T = 17 and 64, N = 4096: 5.2 and 9.1, tiles 8.5 and 9.4). Each 16 columns read all of X again: with
+//                   N = 16384 tiles would be faster (T = 17 and 64: 14.2 and 32.2, tiles 12.6 and 13.2)
 //   up to 160 tiles 64 x 128, two workgroups a CU (T = 400, N = 4096: 9.5; 128 x 128 11.6, 256 x 256 26.5)
 //   up to 512 tiles 128 x 128, two workgroups a CU (T = 1600, N = 4096: 23.4; 64 x 128 33.5, 256 x 256 30.6)
 //   more            256 x 256, one workgroup a CU: half the LDS traffic for each product (T = 3200, N = 4096:

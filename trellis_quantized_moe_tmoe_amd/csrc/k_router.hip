@@ -204,7 +204,8 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_rows(BalanceArgs
   for (int j = 0; j < V; ++j) acc[j] = 0.0f;
   int n = 0;
   // kBatch rows at a time, so that their loads are in flight together (one row at a time: 27.8 us at
-  // T = 32768, E = 256 in bf16); a row that does not count adds zeros whatever it holds
+  // T = 32768, E = 256 in bf16); a row that does not count adds zeros whatever it holds. Up to T = 4096 a wavefront has
+  // one row, and the other three places repeat a row for nothing.
   for (int t0 = beg + wv; t0 < end; t0 += kBalanceWaves * kBatch) {
     float v[kBatch][V], lse[kBatch];
 #pragma unroll

@@ -45,8 +45,7 @@ struct Mxfp4QuantArgs {
   uint8_t* scales;           // [rows][cols / 32]
 };
 
-// Quantises eight neighbouring values (group g); the four lanes of a block exchange their largest magnitude (as
-// integer bits, so infinities and NaNs win) by quad permutes: whole quads call it together.
+// Largest of a quad's four values, by quad permutes.
 __device__ __forceinline__ uint32_t mxfp4_quad_max(uint32_t v) {
   uint32_t o = __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);   // quad_perm 1,0,3,2
   v = o > v ? o : v;
@@ -77,6 +76,8 @@ __device__ __forceinline__ void mxfp4_load8(const void* x, long long g, float (&
   }
 }
 
+// Quantises eight neighbouring values (group g); the four lanes of a block exchange their largest magnitude (as
+// integer bits, so infinities and NaNs win): whole quads call it together.
 template <int DT>
 __device__ __forceinline__ void mxfp4_quantize_group(const Mxfp4QuantArgs& a, long long g) {
   float v[8];
