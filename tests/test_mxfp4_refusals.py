@@ -116,6 +116,21 @@ def test_binding_refuses_what_does_not_fit():
             bad()
 
 
+def test_a_refused_call_leaves_its_output_as_it_was():
+    """Autograd is told that y is written only by a call that writes it."""
+    from trellis_quantized_moe_tmoe_amd import mxfp4
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    plan = mxfp4.ExpertPlan(64, 32, 4, 2, 8)
+    wt = mxfp4.ExpertWeights(u8(4, 64, 32), u8(4, 64, 2), u8(4, 64, 16), u8(4, 64, 1))
+    y = torch.zeros(3, 64)
+    with pytest.raises(ValueError, match="GPU device"):
+        plan.forward(torch.zeros(3, 64, dtype=torch.bfloat16), torch.zeros(3, 2, dtype=torch.int64), torch.zeros(3, 2), wt,
+                     u8(plan.scratch_bytes), y=y)
+    with pytest.raises(ValueError, match="GPU device"):
+        mxfp4.linear(u8(3, 32), u8(3, 2), u8(64, 32), u8(64, 2), y=y)
+    assert y._version == 0
+
+
 def test_gradients_are_refused_not_lost():
     """The calls read addresses and have no backward: a tensor that wants a gradient, in either mode, is refused unless
     gradients are off; the bf16 activations and the router's weights of a training step among them."""

@@ -94,16 +94,18 @@ def linear(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
     if _operand(w_codes, w_scales, "w", 2) != K:
         raise ValueError(f"w: rows of {2 * w_codes.shape[1]} values, x has {K}")
     T, N, out, dev = x_codes.shape[0], w_codes.shape[0], _out_dtype(out_dtype), x_codes.device
-    if y is None:
+    given = y is not None
+    if not given:
         y = torch.empty((T, N), dtype=out_dtype, device=dev)
     else:
         _no_gradient(y=y)
         if not _fits(y, (T, N), out_dtype):
             _require(y, "y", (T, N), (out_dtype,))
-        increment_version(y)                      # a graph that saved y learns that it is written
     if not _one_gpu(x_codes, x_scales, w_codes, w_scales, y):
         _same_device([("x codes", x_codes), ("x scales", x_scales), ("w codes", w_codes), ("w scales", w_scales),
                       ("y", y)])
+    if given:
+        increment_version(y)                      # a graph that saved y learns that it is written
     _launch(dev.index, lib.tmoe_linear_mxfp4, "tmoe_linear_mxfp4", x_codes.data_ptr(), x_scales.data_ptr(), T,
             w_codes.data_ptr(), w_scales.data_ptr(), K, N, out, y.data_ptr())
     return y
@@ -160,10 +162,9 @@ class ExpertPlan:
                 scratch: torch.Tensor, y: Optional[torch.Tensor] = None) -> torch.Tensor:
         """y [T, H] of x bf16 [T, H] (or its bit patterns), ids [T, k], w fp32 [T, k]."""
         _no_gradient(x=x, w=w, y=y)
-        if isinstance(y, torch.Tensor):
-            increment_version(y)                  # a graph that saved y learns that it is written
+        given = y is not None
         T = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else -1
-        if y is None and isinstance(x, torch.Tensor):
+        if not given and isinstance(x, torch.Tensor):
             y = torch.empty((max(T, 0), self.hidden), dtype=self.out_dtype, device=x.device)
         if not (0 <= T <= self.max_tokens and x.shape[1] == self.hidden and x.dtype in _BITS16 and x.is_contiguous()
                 and _fits(ids, (T, self.top_k), self.ids_dtype) and _fits(w, (T, self.top_k), torch.float32)
@@ -174,6 +175,8 @@ class ExpertPlan:
                 and scratch.is_contiguous() and scratch.numel() >= self.scratch_bytes
                 and _one_gpu(x, ids, w, y, scratch, weights.w1, weights.s1, weights.w2, weights.s2)):
             self.check_call(x, ids, w, weights, scratch, y)
+        if given:
+            increment_version(y)                  # a graph that saved y learns that it is written
         _launch(x.get_device(), lib.tmoe_forward_mxfp4, "tmoe_forward_mxfp4", self.handle, x.data_ptr(), ids.data_ptr(),
                 w.data_ptr(), T, ctypes.byref(weights.c), y.data_ptr(), scratch.data_ptr(), scratch.numel())
         return y

@@ -6,7 +6,8 @@ that are not available come out as id -1, which the layer drops.
 
 `topk` and `balance_loss` record a gradient where the logits require one (first derivatives only; tensors with a
 forward-mode tangent are refused). It flows from `w` and `loss`; `lse`, `counts` and `slope` are not differentiable, so
-a loss computed from them trains nothing.
+a loss computed from them trains nothing. The layers are forward only: hand them `w.detach()`, and `w` the gradient
+that the rest of the program has for it.
 `backward` is the same gradient as one explicit call, for programs without autograd and for hipGraph
 capture."""
 from __future__ import annotations
