@@ -348,6 +348,83 @@ tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t plan, const void *x_bf16, const
                                const float *topk_w, int32_t T, const tmoe_mxfp4_weights *weights, void *y,
                                void *scratch, size_t scratch_bytes, void *stream);
 
+/* ---- RMS norm with the residual's addition, and its gradients ----
+ * Rows of H values:
+ *   h = x + residual, rounded to their type (h = x without a residual);  r = 1 / sqrt(mean(h^2) + eps)
+ *   y = h r g                                     in x's type, or in MXFP8 (the operators below)
+ * and from dy and the gradient dh that reaches h from elsewhere (null: none)
+ *   dx = dh + r (g dy - h r^2 mean(g dy h))       the gradient of x and of the residual alike
+ *   dg = sum over rows of dy h r
+ * Sums are held in fp32; every output is rounded once. A row whose squares sum past fp32's largest value gives y = 0,
+ * one with an infinity or a NaN gives NaN. Outputs must not overlap inputs. */
+typedef struct {
+  int32_t hidden;              /* H: 1..16384; MXFP8 output: a multiple of 32                    */
+  int32_t dtype;               /* of x, residual, h, y and their gradients: TMOE_F32, BF16, F16  */
+  int32_t weight_dtype;        /* of g and dg: TMOE_F32 or dtype                                 */
+  float eps;                   /* finite, >= 0                                                   */
+} tmoe_norm_config;
+
+/* x, residual: [T] rows of H values, their strides elements from row to row (>= H); residual may be null, h is then
+ * null too; weight: [H]; y, h: [T][H]; rstd: fp32 [T], r of every row, or null. Pointers aligned to their elements.
+ * T <= 2^22; T = 0 launches nothing. One launch; deterministic. */
+tmoe_status tmoe_rms_norm(const tmoe_norm_config *cfg, const void *x, int64_t x_stride, const void *residual,
+                          int64_t residual_stride, const void *weight, int32_t T, void *y, void *h, float *rstd,
+                          void *stream);
+/* The same with y in MXFP8: codes [T][H] (16-byte aligned) and scales [T][H/32]. */
+tmoe_status tmoe_rms_norm_mxfp8(const tmoe_norm_config *cfg, const void *x, int64_t x_stride, const void *residual,
+                                int64_t residual_stride, const void *weight, int32_t T, uint8_t *codes,
+                                uint8_t *scales, void *h, void *stream);
+/* h: [T] rows, h_stride elements apart; rstd as the forward wrote it; dy, dh (or null), dx: [T][H]; dweight: [H] of
+ * weight_dtype. Scratch: tmoe_rms_norm_backward_scratch bytes, 16-byte aligned, under the scratch rules above. Two
+ * launches, sums in a fixed order; T = 0 writes dweight = 0 (one launch). */
+tmoe_status tmoe_rms_norm_backward_scratch(const tmoe_norm_config *cfg, int32_t T, size_t *scratch_bytes);
+tmoe_status tmoe_rms_norm_backward(const tmoe_norm_config *cfg, const void *h, int64_t h_stride, const void *weight,
+                                   const float *rstd, const void *dy, const void *dh, int32_t T, void *dx,
+                                   void *dweight, void *scratch, size_t scratch_bytes, void *stream);
+
+/* ---- MXFP8 quantisation ----
+ * As MXFP4 above with E4M3 elements: codes [rows][K], one byte a value, scales [rows][K/32], the scale the smallest
+ * power of two (at least 2^-127) with amax / 2^e <= 448. Arguments and limits as for the MXFP4 calls. */
+tmoe_status tmoe_mxfp8_quantize(const void *x, int32_t dtype, int64_t rows, int32_t cols, uint8_t *codes,
+                                uint8_t *scales, void *stream);
+tmoe_status tmoe_mxfp8_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols,
+                                  int32_t dtype, void *x, void *stream);
+
+/* ---- products grouped by expert over ragged rows ----
+ * R rows sorted by expert: expert e has the rows [offsets[e], offsets[e+1]), any number of them, none included.
+ *   linear  y[r][n]     = sum_k x[r][k] w[e][n][k]
+ *   grad_x  dx[r][k]    = sum_n dy[r][n] w[e][n][k]
+ *   grad_w  dw[e][n][k] = sum over e's rows r of dy[r][n] x[r][k]
+ * x, dx: [R][K]; y, dy: [R][N]; w, dw: [E][N][K]. Outputs are fully overwritten: rows in front of offsets[0] and behind
+ * offsets[E] (routes that were dropped, sorted there) get zeros whatever they hold, and so does dw of an expert without
+ * rows. Sums are fp32, rounded once; each value is summed in one order, so repeated calls give identical bits. offsets
+ * is read on the device; it must not descend: otherwise the results are unspecified (nothing outside the arrays is read
+ * or written). */
+typedef struct {
+  int32_t num_experts;         /* E: 1..512                                                      */
+  int32_t in_features;         /* K: a multiple of 8 (MXFP8: of 32), up to 65536                 */
+  int32_t out_features;        /* N: a multiple of 8, up to 65536                                */
+  int32_t dtype;               /* of x, w and dy: TMOE_BF16 or TMOE_F16 (MXFP8: not read)        */
+  int32_t out_dtype;           /* TMOE_F32 or dtype (MXFP8: TMOE_F32 or TMOE_BF16)               */
+  int32_t offsets_dtype;       /* TMOE_IDS_I32 or TMOE_IDS_I64                                   */
+} tmoe_grouped_config;
+
+/* R <= 2^26; R = 0 launches nothing (grad_w: writes zeros). Pointers 16-byte aligned, offsets to their elements. One
+ * launch each; no scratch. UNSUPPORTED also for outputs of more tiles than a launch has workgroups (2^24). */
+tmoe_status tmoe_grouped_linear(const tmoe_grouped_config *cfg, const void *x, const void *w, const void *offsets,
+                                int32_t R, void *y, void *stream);
+tmoe_status tmoe_grouped_grad_x(const tmoe_grouped_config *cfg, const void *dy, const void *w, const void *offsets,
+                                int32_t R, void *dx, void *stream);
+tmoe_status tmoe_grouped_grad_w(const tmoe_grouped_config *cfg, const void *dy, const void *x, const void *offsets,
+                                int32_t R, void *dw, void *stream);
+/* linear with MXFP8 x (codes [R][K], scales [R][K/32]) and w (codes [E][N][K], scales [E][N][K/32]). Codes 16-byte
+ * aligned. The 8-bit matrix unit adds 16 neighbouring products at a time, each cut at 2^-13 of the largest of the 16 (of
+ * its operands' powers of two), and those sums in fp32: an error of at most 2^-9 of the largest product for every 16,
+ * small beside E4M3's own steps of 2^-3; fp32 results are unrounded, not more exact than that. */
+tmoe_status tmoe_grouped_linear_mxfp8(const tmoe_grouped_config *cfg, const uint8_t *x_codes,
+                                      const uint8_t *x_scales, const uint8_t *w_codes, const uint8_t *w_scales,
+                                      const void *offsets, int32_t R, void *y, void *stream);
+
 /* ---- test hooks: expose single steps so their bit-exactness can be graded ---- */
 
 /* Decode expert `expert`'s FC1 (matrix 0, H x 2I) or FC2 (matrix 1, I x H) with the same device

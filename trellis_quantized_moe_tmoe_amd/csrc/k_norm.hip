@@ -1,0 +1,296 @@
+// k_norm.hip -- RMS norm with the residual's addition, its MXFP8 form, and the gradients.
+//
+//   h = x + residual (rounded to their type);  r = 1 / sqrt(mean(h^2) + eps);  y = h r g
+//   dx = dh + r (g dy - h r^2 mean(g dy h));   dg = sum over rows of dy h r
+// Sums are fp32 whatever the types; every output is rounded once. All of it is one pass over the data and bound by HBM
+// for many rows, by one row's latency for few.
+//
+// A row is held in registers by 64 to 1024 threads, vectors of 16 bytes of x a lane (its last vector may be short), so
+// nothing is read twice. Rows may start at any element: the vectors are loaded at the element's alignment.
+#include <algorithm>
+
+#include "tmoe.h"
+#include "tmoe_mxfp8.hpp"
+#include "tmoe_norm.hpp"
+
+namespace tmoe {
+
+namespace {
+
+struct F32 {
+  typedef float T;
+  static constexpr int V = 4;
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+struct BF16 {
+  typedef uint16_t T;
+  static constexpr int V = 8;
+  static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+  static __device__ __forceinline__ uint16_t put(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
+};
+struct F16 {
+  typedef uint16_t T;
+  static constexpr int V = 8;
+  static __device__ __forceinline__ float get(uint16_t v) { return static_cast<float>(__builtin_bit_cast(_Float16, v)); }
+  static __device__ __forceinline__ uint16_t put(float v) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v)); }
+};
+
+// V neighbouring values of a row of H from element `at`; zeros past the end.
+template <class D, int V>
+__device__ __forceinline__ void load_vec(const typename D::T* row, int at, int H, float (&v)[V]) {
+  typename D::T raw[V];
+  if (at + V <= H) {
+    __builtin_memcpy(raw, row + at, sizeof(raw));
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = D::get(raw[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = at + i < H ? D::get(row[at + i]) : 0.0f;
+  }
+}
+template <class D, int V>
+__device__ __forceinline__ void store_vec(typename D::T* row, int at, int H, const float (&v)[V]) {
+  typename D::T raw[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) raw[i] = D::put(v[i]);
+  if (at + V <= H) {
+    __builtin_memcpy(row + at, raw, sizeof(raw));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (at + i < H) row[at + i] = raw[i];
+  }
+}
+
+// Sum over the wavefront, in every lane, in an order that does not depend on the lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#define TMOE_STEP(CTRL, ROWS) \
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+  TMOE_STEP(0x111, 0xF)
+  TMOE_STEP(0x112, 0xF)
+  TMOE_STEP(0x114, 0xF)
+  TMOE_STEP(0x118, 0xF)
+  TMOE_STEP(0x142, 0xA)
+  TMOE_STEP(0x143, 0xC)
+#undef TMOE_STEP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sum over the wavefronts of a row (WIDE: a whole workgroup). sh: 16 values, free for the next sum behind its barrier.
+template <bool WIDE>
+__device__ __forceinline__ float row_sum(float v, float* sh) {
+  v = wave_sum(v);
+  if constexpr (WIDE) {
+    const int waves = blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = sh[0];
+    for (int p = 1; p < waves; ++p) v += sh[p];
+  }
+  return v;
+}
+
+template <class D, class W, int NV, bool WIDE, bool MX>
+__global__ void k_rms_norm(NormArgs a) {
+  constexpr int V = D::V;
+  __shared__ float sh[16];
+  const int H = a.hidden, tid = threadIdx.x, threads = blockDim.x;
+  const int t = blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= a.tokens) return;                     // whole wavefronts; WIDE: the whole workgroup
+  const typename D::T* x = static_cast<const typename D::T*>(a.x) + t * a.x_stride;
+  const typename D::T* res = static_cast<const typename D::T*>(a.residual) + t * a.residual_stride;
+  const long long row = static_cast<long long>(t) * H;
+  float h[NV][V], sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) load_vec<D, V>(x, (j * threads + tid) * V, H, h[j]);
+  if (a.residual) {
+    float r[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_vec<D, V>(res, (j * threads + tid) * V, H, r[j]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[j][i] = D::get(D::put(h[j][i] + r[j][i]));   // as it is stored
+      store_vec<D, V>(static_cast<typename D::T*>(a.h) + row, (j * threads + tid) * V, H, h[j]);
+    }
+  }
+  float g[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) load_vec<W, V>(static_cast<const typename W::T*>(a.weight), (j * threads + tid) * V, H, g[j]);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum = fmaf(h[j][i], h[j][i], sum);
+  sum = row_sum<WIDE>(sum, sh);
+  const float rstd = 1.0f / sqrtf(sum / static_cast<float>(H) + a.eps);
+  if (a.rstd && tid == 0) a.rstd[t] = rstd;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int at = (j * threads + tid) * V;
+    float y[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] = h[j][i] * rstd * g[j][i];
+    if constexpr (MX) {                          // H is a multiple of 32: whole blocks, 4 lanes (16-bit x) or 8 each
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t b = __float_as_uint(y[i]) & 0x7fffffffu;
+        m = b > m ? b : m;
+      }
+      const uint32_t byte = mxfp8_scale_byte(V == 8 ? mxfp4_quad_max(m) : mxfp8_oct_max(m));
+      const float inv = mxfp4_inverse_scale(byte);
+      if (at < H) {
+        uint8_t* codes = static_cast<uint8_t*>(a.y) + row + at;
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const uint32_t c = mxfp8_codes4(y[i] * inv, y[i + 1] * inv, y[i + 2] * inv, y[i + 3] * inv);
+          *reinterpret_cast<uint32_t*>(codes + i) = byte == 255u ? 0u : c;
+        }
+        if (at % 32 == 0) a.scales[(row + at) / 32] = static_cast<uint8_t>(byte);
+      }
+    } else {
+      store_vec<D, V>(static_cast<typename D::T*>(a.y) + row, at, H, y);
+    }
+  }
+}
+
+// One pass over the rows, workgroup g of a.groups every groups-th batch of rows; dweight's sums over its rows stay in
+// registers and leave as one row of partial sums.
+template <class D, class W, int NV, bool WIDE>
+__global__ void k_rms_norm_grad(NormGradArgs a) {
+  constexpr int V = D::V;
+  __shared__ float sh[2][16];
+  const int H = a.hidden, tid = threadIdx.x, threads = blockDim.x, rows = blockDim.y;
+  const typename W::T* w = static_cast<const typename W::T*>(a.weight);
+  float dg[NV][V] = {};
+  int turn = 0;
+  for (long long t = blockIdx.x * rows + threadIdx.y; t < a.tokens; t += static_cast<long long>(a.groups) * rows) {
+    const long long row = t * H;
+    const typename D::T* hp = static_cast<const typename D::T*>(a.h) + t * a.h_stride;
+    float h[NV][V], d[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      load_vec<D, V>(hp, (j * threads + tid) * V, H, h[j]);
+      load_vec<D, V>(static_cast<const typename D::T*>(a.dy) + row, (j * threads + tid) * V, H, d[j]);
+    }
+    const float r = a.rstd[t];
+    float c = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float g[V];
+      load_vec<W, V>(w, (j * threads + tid) * V, H, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        h[j][i] *= r;                            // the row's unit values
+        dg[j][i] = fmaf(d[j][i], h[j][i], dg[j][i]);
+        d[j][i] *= g[i];
+        c = fmaf(d[j][i], h[j][i], c);
+      }
+    }
+    c = row_sum<WIDE>(c, sh[turn]) / static_cast<float>(H);
+    turn ^= 1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int at = (j * threads + tid) * V;
+      float o[V] = {};
+      if (a.dh) load_vec<D, V>(static_cast<const typename D::T*>(a.dh) + row, at, H, o);
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = fmaf(r, fmaf(-h[j][i], c, d[j][i]), o[i]);
+      store_vec<D, V>(static_cast<typename D::T*>(a.dx) + row, at, H, o);
+    }
+  }
+  float* part = a.part + static_cast<long long>(blockIdx.x * rows + threadIdx.y) * H;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) store_vec<F32, V>(part, (j * threads + tid) * V, H, dg[j]);
+}
+
+// dweight: 64 columns a workgroup, its 16 wavefronts every 16th partial row, joined in a fixed order.
+template <class W>
+__global__ __launch_bounds__(1024) void k_rms_norm_dweight(const float* part, int n, int H, void* dweight) {
+  __shared__ float sh[16][64];
+  const int c = blockIdx.x * 64 + threadIdx.x, at = min(c, H - 1);
+  float s = 0.0f;
+  for (int p = threadIdx.y; p < n; p += 16) s += part[static_cast<long long>(p) * H + at];
+  sh[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < H) {
+    for (int p = 1; p < 16; ++p) s += sh[p][threadIdx.x];
+    static_cast<typename W::T*>(dweight)[c] = W::put(s);
+  }
+}
+
+template <class D, class W, bool MX>
+void launch_norm(const NormArgs& a, int dtype, hipStream_t s) {
+  const NormShape n = norm_shape(a.hidden, dtype);
+  const dim3 g((a.tokens + n.rows - 1) / n.rows), b(n.threads, n.rows);
+  if (n.threads == 64) {
+    if (n.nv == 1) hipLaunchKernelGGL((k_rms_norm<D, W, 1, false, MX>), g, b, 0, s, a);
+    else if (n.nv == 2) hipLaunchKernelGGL((k_rms_norm<D, W, 2, false, MX>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((k_rms_norm<D, W, 4, false, MX>), g, b, 0, s, a);
+  } else {
+    if (n.nv == 1) hipLaunchKernelGGL((k_rms_norm<D, W, 1, true, MX>), g, b, 0, s, a);
+    else if (n.nv == 2) hipLaunchKernelGGL((k_rms_norm<D, W, 2, true, MX>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((k_rms_norm<D, W, 4, true, MX>), g, b, 0, s, a);
+  }
+}
+
+template <class D, class W>
+void launch_grad(const NormGradArgs& a, int dtype, hipStream_t s) {
+  const NormShape n = norm_shape(a.hidden, dtype);
+  const dim3 g(a.groups), b(n.threads, n.rows);
+  if (a.groups == 0) {
+  } else if (n.threads == 64) {
+    if (n.nv == 1) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, false>), g, b, 0, s, a);
+    else if (n.nv == 2) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 2, false>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((k_rms_norm_grad<D, W, 4, false>), g, b, 0, s, a);
+  } else {
+    if (n.nv == 1) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, true>), g, b, 0, s, a);
+    else if (n.nv == 2) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 2, true>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((k_rms_norm_grad<D, W, 4, true>), g, b, 0, s, a);
+  }
+  hipLaunchKernelGGL((k_rms_norm_dweight<W>), dim3((a.hidden + 63) / 64), dim3(64, 16), 0, s, a.part, a.groups * n.rows,
+                     a.hidden, a.dweight);
+}
+
+}  // namespace
+
+NormShape norm_shape(int hidden, int dtype) {
+  const int v = dtype == TMOE_F32 ? 4 : 8, vecs = (hidden + v - 1) / v;
+  NormShape n;
+  if (vecs <= 256) {
+    n.threads = 64;
+    n.rows = 4;
+    n.nv = vecs <= 64 ? 1 : vecs <= 128 ? 2 : 4;
+  } else {
+    n.rows = 1;
+    n.nv = vecs <= 2048 ? 2 : 4;
+    n.threads = ((vecs + n.nv - 1) / n.nv + 63) / 64 * 64;
+  }
+  return n;
+}
+
+int norm_grad_groups(int tokens, int hidden, int dtype) {
+  const NormShape n = norm_shape(hidden, dtype);
+  return std::max(1, std::min((tokens + n.rows - 1) / n.rows, 1024));
+}
+
+void launch_rms_norm(const NormArgs& a, int dtype, bool weight_f32, bool mxfp8, hipStream_t s) {
+  auto go = [&](auto d, auto w) {
+    using D = decltype(d);
+    using W = decltype(w);
+    if (mxfp8) launch_norm<D, W, true>(a, dtype, s);
+    else launch_norm<D, W, false>(a, dtype, s);
+  };
+  if (dtype == TMOE_F32) go(F32{}, F32{});
+  else if (dtype == TMOE_BF16) weight_f32 ? go(BF16{}, F32{}) : go(BF16{}, BF16{});
+  else weight_f32 ? go(F16{}, F32{}) : go(F16{}, F16{});
+}
+
+void launch_rms_norm_grad(const NormGradArgs& a, int dtype, bool weight_f32, hipStream_t s) {
+  if (dtype == TMOE_F32) launch_grad<F32, F32>(a, dtype, s);
+  else if (dtype == TMOE_BF16) weight_f32 ? launch_grad<BF16, F32>(a, dtype, s) : launch_grad<BF16, BF16>(a, dtype, s);
+  else weight_f32 ? launch_grad<F16, F32>(a, dtype, s) : launch_grad<F16, F16>(a, dtype, s);
+}
+
+}  // namespace tmoe

@@ -29,7 +29,10 @@ EXPORTS = ["tmoe_plan", "tmoe_plan_destroy", "tmoe_plan_get_info", "tmoe_plan_ex
            "tmoe_linear_plan", "tmoe_linear_plan_destroy", "tmoe_linear_w4a16",
            "tmoe_router_topk", "tmoe_balance_loss_scratch", "tmoe_balance_loss", "tmoe_router_backward",
            "tmoe_mxfp4_quantize", "tmoe_mxfp4_dequantize", "tmoe_linear_mxfp4", "tmoe_mxfp4_plan",
-           "tmoe_mxfp4_plan_destroy", "tmoe_forward_mxfp4"]
+           "tmoe_mxfp4_plan_destroy", "tmoe_forward_mxfp4",
+           "tmoe_rms_norm", "tmoe_rms_norm_mxfp8", "tmoe_rms_norm_backward_scratch", "tmoe_rms_norm_backward",
+           "tmoe_mxfp8_quantize", "tmoe_mxfp8_dequantize",
+           "tmoe_grouped_linear", "tmoe_grouped_grad_x", "tmoe_grouped_grad_w", "tmoe_grouped_linear_mxfp8"]
 
 
 class Config(ctypes.Structure):
@@ -85,6 +88,16 @@ class Mxfp4Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "s1", "w2", "s2")]
 
 
+class NormConfig(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class GroupedConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_experts", "in_features", "out_features", "dtype", "out_dtype",
+                                              "offsets_dtype")]
+
+
 class TmoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}")
@@ -134,6 +147,16 @@ def _load():
     lib.tmoe_mxfp4_plan.argtypes = [ctypes.POINTER(Mxfp4Config), ctypes.POINTER(P), ctypes.POINTER(SZ)]
     lib.tmoe_mxfp4_plan_destroy.argtypes = [P]
     lib.tmoe_forward_mxfp4.argtypes = [P, P, P, P, I32, ctypes.POINTER(Mxfp4Weights), P, P, SZ, P]
+    NC, GC = ctypes.POINTER(NormConfig), ctypes.POINTER(GroupedConfig)
+    lib.tmoe_rms_norm.argtypes = [NC, P, I64, P, I64, P, I32, P, P, P, P]
+    lib.tmoe_rms_norm_mxfp8.argtypes = [NC, P, I64, P, I64, P, I32, P, P, P, P]
+    lib.tmoe_rms_norm_backward_scratch.argtypes = [NC, I32, ctypes.POINTER(SZ)]
+    lib.tmoe_rms_norm_backward.argtypes = [NC, P, I64, P, P, P, P, I32, P, P, P, SZ, P]
+    lib.tmoe_mxfp8_quantize.argtypes = [P, I32, I64, I32, P, P, P]
+    lib.tmoe_mxfp8_dequantize.argtypes = [P, P, I64, I32, I32, P, P]
+    for fn in (lib.tmoe_grouped_linear, lib.tmoe_grouped_grad_x, lib.tmoe_grouped_grad_w):
+        fn.argtypes = [GC, P, P, P, I32, P, P]
+    lib.tmoe_grouped_linear_mxfp8.argtypes = [GC, P, P, P, P, P, I32, P, P]
     for name in EXPORTS:
         if name != "tmoe_status_str":
             getattr(lib, name).restype = I32
