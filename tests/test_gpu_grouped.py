@@ -103,6 +103,25 @@ def test_fp32_results_and_64_bit_offsets(sizes, K, N, front, back, dtype):
     Case(sizes, K, N, dtype, front, back, ids=torch.int64).all(torch.float32)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_256_x_256_tiles(dtype):
+    """Rows and outputs large enough for the largest tiles: odd depths, short last tiles, rows outside, both output types."""
+    for out in (None, torch.float32):
+        Case([700, 0, 341], 200, 10008, dtype, 3, 300).linear(out)
+        Case([513], 8, 16392, dtype).linear(out)
+        Case([700, 0, 341], 10008, 136, dtype, 3, 300).grad_x(out)
+        Case([513], 16392, 72, dtype).grad_x(out)
+        Case([700, 331], 2312, 2568, dtype, 5, 9).grad_w(out)
+        Case([1100, 0, 37, 950], 1800, 1544, dtype).grad_w(out)
+
+
+def test_popular_experts_first():
+    """grad_w takes experts with more than three times the average first: none, one, as many as there can be, and the last one."""
+    for sizes in ([40] * 9, [1200] + [0] * 30, [0] * 40 + [1500], [300, 0, 0, 0] * 8 + [1], [0, 0, 0, 900, 4, 4, 4, 700] * 3,
+                  [33] * 65 + [3000] + [20] * 70):
+        Case(sizes, 136, 72, torch.bfloat16, 1, 1).grad_w()
+
+
 def test_many_experts():
     rng = np.random.default_rng(1)
     for E, top in ((511, 3), (512, 60), (300, 9)):
@@ -272,7 +291,24 @@ def test_mxfp8(sizes, N, front, back, K):
         assert torch.all(y[out] == 0)
 
 
-@pytest.mark.parametrize("sizes,K,N", [([1, 0, 40], 32, 24), ([30, 2, 70], 96, 136), ([500], 1088, 264), ([2000, 9], 640, 72)])
+def test_mxfp8_256_x_256_tiles():
+    off, R = _offsets([1100, 0, 700], 3, 9)
+    for K, N in ((512, 10008), (896, 8200), (2304, 8200)):
+        gen = torch.Generator(device="cuda").manual_seed(K)
+        (xq, xs), (wq, ws) = (_mx().quantize(torch.randn(*s, generator=gen, device="cuda")) for s in ((R, K), (3, N, K)))
+        y = _mx().grouped_linear(xq, xs, wq, ws, torch.from_numpy(off).cuda(), torch.float32)
+        x, w = _mx().dequantize(xq, xs).double(), _mx().dequantize(wq, ws).double()
+        px, pw = (torch.exp2(torch.floor(torch.log2(t.abs().clamp(min=2.0 ** -40)))) for t in (x, w))
+        for e in (0, 2):
+            a, b = int(off[e]), int(off[e + 1])
+            ref, s = x[a:b] @ w[e].t(), x[a:b].abs() @ w[e].abs().t()
+            # the cut of 16 products is at most 2^-9 of their largest, which is at most the sum of all (mxfp8_ref.cut_bound)
+            bound = 2 * M.U * (K + 4) * s + 2.0 ** -9 * (px[a:b] @ pw[e].t())
+            assert bool(((y[a:b].double() - ref).abs() <= bound).all())
+        assert torch.all(y[:3] == 0) and torch.all(y[-9:] == 0)
+
+
+@pytest.mark.parametrize("sizes,K,N", [([1, 0, 40], 32, 24), ([30, 2, 70], 96, 136), ([500], 1088, 264), ([2000, 9], 640, 72), ([1040], 640, 10008)])
 def test_mxfp8_products_of_one_size_are_exact(sizes, K, N):
     """Values 1, 2 and 3 times a power of two by blocks: nothing is cut and every sum fits fp32, so every product counts."""
     off, R = _offsets(sizes)

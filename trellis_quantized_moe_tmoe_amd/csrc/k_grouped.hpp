@@ -47,25 +47,29 @@ __device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 7) ^ ((r & 1)
 constexpr int kRsrcFlags = 0x00027000;           // raw buffer, 32-bit data
 constexpr int kPastEnd = static_cast<int>(0x80000000u);   // an offset outside every buffer
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, long long bytes) {
-  const int n = static_cast<int>(bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : bytes);
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, n, kRsrcFlags);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, max(bytes, 0), kRsrcFlags);
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <int KIND, int WT_, int WC_, int MT_, int NT_, int SLOTS_>
+// SCALES (MXFP8): 4 copies the scales of four slots at a time, 1 of one slot; 0: no copies (byte loads).
+// DEPTH: depth of a slot; 128 bytes, or less where both operands are KS.
+template <int KIND, int WT_, int WC_, int MT_, int NT_, int SLOTS_, int SCALES_ = 0, int DEPTH_ = KIND == kKindMx8 ? 128 : 64>
 struct GTile {
+  static constexpr int SCALES = SCALES_;
   static constexpr int WT = WT_, WC = WC_, MT = MT_, NT = NT_, SLOTS = SLOTS_;
   static constexpr int ES = KIND == kKindMx8 ? 1 : 2;             // bytes a value
-  static constexpr int DEPTH = 128 / ES;                          // depth of a slot
+  static constexpr int DEPTH = DEPTH_;
   static constexpr int TR = 32 * MT * WT, TC = 32 * NT * WC;
-  static constexpr int kSlot = (TR + TC) * 128;
-  static constexpr int kScaleRows = KIND == kKindMx8 ? TC + (TR + 63) / 64 * 64 : 0;
-  static constexpr int kScaleSlot = 4 * kScaleRows;               // a dword a row
-  static constexpr int kLds = SLOTS * (kSlot + kScaleSlot);
-  static constexpr int SPW = (kScaleRows / 64 + 3) / 4;           // scale copies a wavefront and slot
-  static constexpr int COPIES = (TR + TC) / 32 + SPW;             // copies a wavefront issues a slot
+  static constexpr int kSlot = (TR + TC) * DEPTH * ES;
+  static constexpr int kScaleRows = SCALES ? TC + (TR + 63) / 64 * 64 : 0;
+  static constexpr int kScaleBuffer = 4 * SCALES * kScaleRows;    // one of two
+  static constexpr int kRing = SLOTS * kSlot;
+  static constexpr int kLds = kRing + 2 * kScaleBuffer;
+  static constexpr int SPW = (kScaleRows / 64 + 3) / 4;           // scale copies of a wavefront
+  static constexpr int COPIES = kSlot / 4096;                     // copies a wavefront issues a slot
+  static_assert(SLOTS == 2 || !SCALES, "two buffers of scales");
   static_assert(WT * WC == 4, "four wavefronts");
 };
 
@@ -111,17 +115,18 @@ __device__ __forceinline__ i4v tr_read(lds_u8* p, int next) {
 }
 
 // One operand's copies: T rows (KC) or columns (KS) of a tile.
-template <int T, bool KS, int ES>
+template <int T, bool KS, int ES, int DEPTH>
 struct Operand {
+  static_assert(KS || DEPTH * ES == 128, "whole lines");
   const uint8_t* base;       // KC: first row; KS: first depth row
-  long long pitch;           // bytes from row to row
+  int pitch;                 // bytes from row to row, at most 2^17
   int rows;                  // KC: rows that exist; KS: depth rows that exist
   int depth_bytes;           // KC: bytes of a row
   int first;                 // offset of copy 0 of this lane
   int step;                  // from copy to copy
   int at;                    // KC: this lane's byte within the slot's 128
 
-  static constexpr int N = T / 32;               // copies a wavefront and slot
+  static constexpr int N = T * DEPTH * ES / 4096;   // copies a wavefront and slot
 
   __device__ __forceinline__ void point(const uint8_t* p, int pitch_bytes, int n, int depth, int col0, int width, int wv, int lane) {
     pitch = pitch_bytes;
@@ -144,11 +149,10 @@ struct Operand {
   }
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(int slot) const {
     if constexpr (KS) {
-      const long long from = 64LL * slot;
-      const long long n = rows - from;
-      return rsrc(base + from * pitch, (n < 64 ? n : 64) * pitch);
+      const int n = rows - DEPTH * slot;
+      return rsrc(base + static_cast<long long>(DEPTH) * slot * pitch, min(n, DEPTH) * pitch);
     } else {
-      return rsrc(base + 128LL * slot, static_cast<long long>(rows) * pitch - 128LL * slot);
+      return rsrc(base + 128LL * slot, rows * pitch - 128 * slot);
     }
   }
   // offset of copy i; behind the row's end: outside
@@ -158,17 +162,17 @@ struct Operand {
   }
 };
 
-template <int KIND, bool RKS, bool CKS, class S, int OUT, bool SCALES4>
+template <int KIND, bool RKS, bool CKS, class S, int OUT>
 __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const GroupedTile& t, uint8_t* lds) {
   constexpr bool MX = KIND == kKindMx8;
-  constexpr int MT = S::MT, NT = S::NT, SUBS = MX ? 2 : 4;
+  constexpr int MT = S::MT, NT = S::NT, SUBS = MX ? 2 : S::DEPTH / 16;
   const int tid = threadIdx.x, lane = tid & 63, wv = uniform(tid >> 6);
   const int r32 = lane & 31, h = lane >> 5, wt = wv / S::WC, wc = wv % S::WC;
   const int row_pitch = (RKS ? a.out_rows : a.depth) * S::ES;
   const int col_pitch = (CKS ? a.cols : a.depth) * S::ES;
 
-  Operand<S::TR, RKS, S::ES> R;
-  Operand<S::TC, CKS, S::ES> C;
+  Operand<S::TR, RKS, S::ES, S::DEPTH> R;
+  Operand<S::TC, CKS, S::ES, S::DEPTH> C;
   const uint8_t* rp = static_cast<const uint8_t*>(a.r);
   const uint8_t* cp = static_cast<const uint8_t*>(a.c);
   if constexpr (RKS) R.point(rp + static_cast<long long>(t.k0) * row_pitch, row_pitch, t.depth, 0, t.row0, a.out_rows, wv, lane);
@@ -182,19 +186,25 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
   const int slots = t.zero ? 0 : (t.depth + S::DEPTH - 1) / S::DEPTH;
 
   lds_u8* const ring = (lds_u8*)lds;
-  auto issue = [&](int slot, int place, int i, __amdgpu_buffer_rsrc_t rr, __amdgpu_buffer_rsrc_t cr) {
+  int islot = 0;                                 // the slot that is copied
+  auto issue = [&](int place, int i, __amdgpu_buffer_rsrc_t rr, __amdgpu_buffer_rsrc_t cr) __attribute__((always_inline)) {
     if (i < C.N)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(cr, (__attribute__((address_space(3))) void*)(ring + place * S::kSlot + S::TR * 128 + (wv + 4 * i) * 1024),
-                                               16, C.offset(slot, i), 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(cr, (__attribute__((address_space(3))) void*)(ring + place * S::kSlot + S::TR * S::DEPTH * S::ES + (wv + 4 * i) * 1024),
+                                               16, C.offset(islot, i), 0, 0, 0);
     else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, (__attribute__((address_space(3))) void*)(ring + place * S::kSlot + (wv + 4 * (i - C.N)) * 1024),
-                                               16, R.offset(slot, i - C.N), 0, 0, 0);
+                                               16, R.offset(islot, i - C.N), 0, 0, 0);
   };
-  // MXFP8 scales, four bytes a row and slot: columns first, then rows. SCALES4: rows of whole dwords, copied like the codes.
+  // MXFP8 scales, columns first, then rows, in two buffers: with the first slot of every four (S::SCALES = 4) 16 bytes a row,
+  // the last ones of a row starting where they end with it (one slot at a time, 4 bytes a row, asks L2 for as many lines as
+  // the codes: 535 us instead of 519 at 8192 x 8192 x 8192).
   const int nblk = MX ? a.depth / 32 : 0;
-  auto issue_scales = [&](int slot, int place) {
-    if constexpr (MX && SCALES4) {
+  auto scales_from = [&](int slot) __attribute__((always_inline)) { return S::SCALES == 4 ? min(4 * slot, nblk - 16) : 4 * slot; };
+  auto issue_scales = [&]() __attribute__((always_inline)) {
+    if constexpr (S::SCALES > 0) {
+      if (S::SCALES > 1 && islot % S::SCALES != 0) return;
       constexpr int CN = S::TC / 64, ALL = S::kScaleRows / 64;
+      const int from = scales_from(islot);
 #pragma unroll
       for (int i = 0; i < S::SPW; ++i) {
         const int j = min(wv + 4 * i, ALL - 1);
@@ -202,17 +212,23 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
         const int row = 64 * (col ? j : j - CN) + lane, n = col ? min(S::TC, a.cols - t.col0) : t.nrows;
         const uint8_t* p = col ? a.cs + (t.expert * a.cols + t.col0) * nblk : a.rs + static_cast<long long>(t.row0) * nblk;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rsrc(p + 4LL * slot, static_cast<long long>(n) * nblk - 4LL * slot),
-            (__attribute__((address_space(3))) void*)(ring + S::SLOTS * S::kSlot + place * S::kScaleSlot + 256 * j), 4,
-            4 * slot < nblk ? row * nblk : kPastEnd, 0, 0, 0);
+            rsrc(p + from, n * nblk - from),
+            (__attribute__((address_space(3))) void*)(ring + S::kRing + islot / S::SCALES % 2 * S::kScaleBuffer + 256 * S::SCALES * j),
+            4 * S::SCALES, row * nblk, 0, 0, 0);
       }
     }
+  };
+  auto scales_at = [&](int slot, int row) __attribute__((always_inline)) {
+    typedef __attribute__((address_space(3))) int lds_i;
+    return *(lds_i*)(ring + S::kRing + slot / max(S::SCALES, 1) % 2 * S::kScaleBuffer + 4 * S::SCALES * row +
+                     (S::SCALES == 4 ? 4 * slot - scales_from(slot / 4 * 4) : 0));
   };
 
   struct Frags {
     i4v r[MT][MX ? 2 : 1], c[NT][MX ? 2 : 1];
     int rs[MT], cs[NT];
   };
+  // Row fragment m of a wavefront is the tile's (m WT + wt)-th, so that short tiles need few of every wavefront's.
   // An 8-bit operand of the 32x32x64 instruction: half h of the wavefront holds the bytes 16 h .. of both 32-blocks, and the
   // scale of block h.
   // KC: places of this lane's chunks; KS: byte offset of its first value, by fragment
@@ -228,7 +244,7 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
     const int in = 16 * (2 * g + ((i & 3) >> 1)) + 8 * (i & 1);
     if constexpr (RKS) {
 #pragma unroll
-      for (int f = 0; f < MT; ++f) tr_r[f] = k * 2 * S::TR + 64 * ((wt * MT + f) ^ m) + in;
+      for (int f = 0; f < MT; ++f) tr_r[f] = k * 2 * S::TR + 64 * ((f * S::WT + wt) ^ m) + in;
     }
     if constexpr (CKS) {
 #pragma unroll
@@ -236,19 +252,18 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
     }
   }
   typedef __attribute__((address_space(3))) i4v lds_i4;
-  typedef __attribute__((address_space(3))) int lds_i;
   // unaligned scales: straight from global memory, a byte a block
-  auto scale_bytes = [&](const uint8_t* p, int n, int row, int slot) {
+  auto scale_bytes = [&](const uint8_t* p, int n, int row, int slot) __attribute__((always_inline)) {
     const uint8_t* q = p + static_cast<long long>(min(row, n - 1)) * nblk;
     int w = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) w |= 4 * slot + b < nblk ? q[4 * slot + b] << (8 * b) : 0;
     return w;
   };
-  auto read_piece = [&](int slot, int place, int s, int p, Frags& f) {
+  auto read_piece = [&](int slot, int place, int s, int p, Frags& f) __attribute__((always_inline)) {
     lds_u8* const base = ring + place * S::kSlot;
     if (p < NT) {
-      lds_u8* const at = base + S::TR * 128;
+      lds_u8* const at = base + S::TR * S::DEPTH * S::ES;
       if constexpr (CKS) {
         f.c[p][0] = tr_read(at + tr_c[p] + s * 16 * 2 * S::TC, 4 * 2 * S::TC);
       } else {
@@ -259,9 +274,9 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
           if (s == 0) {
             const int row = 32 * (wc * NT + p) + r32;
             int w;
-            if constexpr (SCALES4) w = *(lds_i*)(ring + S::SLOTS * S::kSlot + place * S::kScaleSlot + 4 * row);
+            if constexpr (S::SCALES > 0) w = scales_at(slot, row);
             else w = scale_bytes(a.cs + (t.expert * a.cols + t.col0) * nblk, a.cols - t.col0, row, slot);
-            f.cs[p] = static_cast<int>(static_cast<uint32_t>(w) >> (8 * h));
+            f.cs[p] = w;
           }
         } else {
           f.c[p][0] = *(lds_i4*)(at + fr + chunk_at[s]);
@@ -272,16 +287,16 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
       if constexpr (RKS) {
         f.r[m][0] = tr_read(base + tr_r[m] + s * 16 * 2 * S::TR, 4 * 2 * S::TR);
       } else {
-        const int fr = 4096 * (wt * MT + m);
+        const int fr = 4096 * (m * S::WT + wt);
         if constexpr (MX) {
           f.r[m][0] = *(lds_i4*)(base + fr + chunk_at[2 * s]);
           f.r[m][1] = *(lds_i4*)(base + fr + chunk_at[2 * s + 1]);
           if (s == 0) {
-            const int row = 32 * (wt * MT + m) + r32;
+            const int row = 32 * (m * S::WT + wt) + r32;
             int w;
-            if constexpr (SCALES4) w = *(lds_i*)(ring + S::SLOTS * S::kSlot + place * S::kScaleSlot + 4 * (S::TC + row));
+            if constexpr (S::SCALES > 0) w = scales_at(slot, S::TC + row);
             else w = scale_bytes(a.rs + static_cast<long long>(t.row0) * nblk, t.nrows, row, slot);
-            f.rs[m] = static_cast<int>(static_cast<uint32_t>(w) >> (8 * h));
+            f.rs[m] = w;
           }
         } else {
           f.r[m][0] = *(lds_i4*)(base + fr + chunk_at[s]);
@@ -295,249 +310,337 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = f16v{};
-
+  constexpr int MM = MT * NT, RD = MT + NT, CP = Operand<S::TR, RKS, S::ES, S::DEPTH>::N + Operand<S::TC, CKS, S::ES, S::DEPTH>::N;
+  // A slot's P = SUBS * MM matrix instructions are positions 0 .. P - 1. In front of position kFree every wavefront has read all of
+  // the slot: the copies that take its place start there; in front of kLanded the next slot's copies have landed and it may be
+  // read. In 256 x 256 tiles (one wavefront a SIMD: nothing else hides what it waits for) the two are barriers of their own, as
+  // far apart as the fragments' registers allow, and a copy goes out every kEvery positions (all at once they stand in each
+  // other's way and hold up the matrix instructions behind them); those past P belong to the next round of the loop.
+  constexpr int P = SUBS * MM;
+  constexpr bool APART = MM == 16;
+  constexpr int kFree = APART ? P - MM - (MX ? 2 : 6) : P - MM, kLanded = APART ? P - MM / 2 : kFree, kEvery = MX ? 1 : 3;
+  auto position = [](int i) { return APART ? kFree + i * kEvery : kFree + i * MM / CP; };
+  auto copies_below = [position](int q) {
+    int n = 0;
+    for (int i = 0; i < CP; ++i) n += position(i) < q;
+    return n;
+  };
+  constexpr int kFirst = copies_below(P), kNewer = (S::SLOTS - 2) * S::COPIES + copies_below(kLanded);
+  static_assert(position(CP - 1) < P + kFree, "a slot's copies have gone out when the next one's start");
+  // fragments in the order in which the matrix instructions want them
+  auto piece = [](int p) { return p == 0 ? 0 : p == 1 ? NT : p <= NT ? p - 1 : p; };
   if (slots > 0) {
-#pragma unroll
-    for (int d = 0; d < S::SLOTS; ++d) {
-      issue_scales(d, d);
-      const auto rr = R.window(d), cr = C.window(d);
-#pragma unroll
-      for (int i = 0; i < R.N + C.N; ++i) issue(d, d, i, rr, cr);
-    }
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S::SLOTS - 1) * S::COPIES) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    int place = 0, into = S::SLOTS - 1;          // the place that is read, the one that is written
+    __amdgpu_buffer_rsrc_t rr, cr;
     Frags f[2];
 #pragma unroll
+    for (int d = 0; d < S::SLOTS; ++d) {
+      islot = d;
+      issue_scales();
+      rr = R.window(d), cr = C.window(d);
+#pragma unroll
+      for (int i = 0; i < (d == S::SLOTS - 1 ? kFirst : CP); ++i) issue(d, i, rr, cr);
+    }
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S::SLOTS - 2) * S::COPIES + kFirst) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
     for (int p = 0; p < MT + NT; ++p) read_piece(0, 0, 0, p, f[0]);
-    constexpr int MM = MT * NT, RD = MT + NT, CP = R.N + C.N;
-    int place = 0;
+    const int fragments = (t.nrows + 32 * S::WT - 1) / (32 * S::WT);
     for (int slot = 0; slot < slots; ++slot) {
       const int next = place + 1 == S::SLOTS ? 0 : place + 1;
       int rs[MT], cs[NT];
       if constexpr (MX) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) rs[m] = f[0].rs[m];
+        for (int m = 0; m < MT; ++m) rs[m] = static_cast<int>(static_cast<uint32_t>(f[0].rs[m]) >> (8 * h));   // bytes 0 and 2: this half's
 #pragma unroll
-        for (int n = 0; n < NT; ++n) cs[n] = f[0].cs[n];
+        for (int n = 0; n < NT; ++n) cs[n] = static_cast<int>(static_cast<uint32_t>(f[0].cs[n]) >> (8 * h));
       }
-      const auto rr = R.window(slot + S::SLOTS), cr = C.window(slot + S::SLOTS);
 #pragma unroll
       for (int s = 0; s < SUBS; ++s) {
-        Frags &cur = f[s & 1], &nxt = f[(s + 1) & 1];
+        Frags &now = f[s & 1], &nxt = f[(s + 1) & 1];
         const bool last = s == SUBS - 1;
-        if (last) {
-          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S::SLOTS - 2) * S::COPIES) : "memory");
-          __builtin_amdgcn_s_barrier();
-          asm volatile("" ::: "memory");
-          issue_scales(slot + S::SLOTS, place);
-        }
 #pragma unroll
         for (int j = 0; j < MM; ++j) {
-          constexpr int per = (RD + MM - 1) / MM;
-#pragma unroll
-          for (int p = j * per; p < (j + 1) * per && p < RD; ++p)
-            read_piece(last ? slot + 1 : slot, last ? next : place, last ? 0 : s + 1, p, nxt);
-          if (last) {
-#pragma unroll
-            for (int i = j * CP / MM; i < (j + 1) * CP / MM; ++i) issue(slot + S::SLOTS, place, i, rr, cr);
+          const int q = s * MM + j;
+          if (q == kFree) {
+            if constexpr (APART) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kNewer) : "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            islot = slot + S::SLOTS;             // past the last one: zeros, which nobody reads
+            into = place;
+            rr = R.window(islot), cr = C.window(islot);
           }
+          if (q == kLanded) {
+            if constexpr (APART) {
+              asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kNewer) : "memory");
+              __builtin_amdgcn_s_barrier();
+              asm volatile("" ::: "memory");
+            }
+            issue_scales();
+          }
+          const int from = last && APART ? MM / 2 : 0;
+          const int per = (RD + MM - from - 1) / (MM - from);
+#pragma unroll
+          for (int p = (j - from) * per; j >= from && p < (j - from + 1) * per && p < RD; ++p)
+            read_piece(last ? slot + 1 : slot, last ? next : place, last ? 0 : s + 1, piece(p), nxt);
+#pragma unroll
+          for (int i = 0; i < CP; ++i)
+            if (position(i) % P == q) issue(into, i, rr, cr);
           __builtin_amdgcn_sched_barrier(0);
           const int m = j / NT, n = j % NT;
           if constexpr (MX) {
-            const i8v c8 = __builtin_shufflevector(cur.c[n][0], cur.c[n][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            const i8v r8 = __builtin_shufflevector(cur.r[m][0], cur.r[m][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            // rows that a short tile does not have are left out (16-bit values: the branches cost full tiles a tenth)
+            if (m >= fragments) continue;
+            const i8v c8 = __builtin_shufflevector(now.c[n][0], now.c[n][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            const i8v r8 = __builtin_shufflevector(now.r[m][0], now.r[m][1], 0, 1, 2, 3, 4, 5, 6, 7);
             acc[m][n] = s == 0 ? mma8<0>(c8, cs[n], r8, rs[m], acc[m][n]) : mma8<1>(c8, cs[n], r8, rs[m], acc[m][n]);
           } else {
-            acc[m][n] = mma<KIND>(cur.c[n][0], cur.r[m][0], acc[m][n]);
+            acc[m][n] = mma<KIND>(now.c[n][0], now.r[m][0], acc[m][n]);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       place = next;
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // copies past the end land before LDS is used again
   }
 
-  // Results leave through the wavefront's own part of LDS, 32 rows at a time, so that a store covers whole rows.
-  constexpr int OS = OUT == TMOE_F32 ? 4 : 2, EPL = 16 / OS, PITCH = 32 * NT * OS + 16;
-  static_assert(4 * 32 * PITCH <= S::kLds, "four wavefronts' rows fit the ring");
-  const int wcol = t.col0 + 32 * NT * wc;
-  uint8_t* y = static_cast<uint8_t*>(a.y);
-  if constexpr (RKS) y += t.expert * a.out_rows * a.cols * OS;
-  __syncthreads();
-  uint8_t* mine = lds + wv * 32 * PITCH;
+      // Results leave through the wavefront's own part of LDS, 32 rows and 128 bytes of them at a time, so that a store covers
+      // whole lines.
+      constexpr int OS = OUT == TMOE_F32 ? 4 : 2, NC = NT == 1 || OUT == TMOE_F32 ? 1 : 2, PITCH = 32 * NC * OS + 16;
+      static_assert(4 * 32 * PITCH <= S::kLds, "four wavefronts' rows fit the ring");
+      const int wcol = t.col0 + 32 * NT * wc;
+      uint8_t* y = static_cast<uint8_t*>(a.y);
+      if constexpr (RKS) y += t.expert * a.out_rows * a.cols * OS;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // copies past the end land before the ring is used again
+      __syncthreads();
+      uint8_t* mine = lds + wv * 32 * PITCH;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+      for (int m = 0; m < MT; ++m) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int n0 = 0; n0 < NT; n0 += NC) {
+          if constexpr (MM == 16) {                // 256 sums a lane: they stay where they are until their turn, or they spill
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f4 v = {acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
-        uint8_t* to = mine + r32 * PITCH + (32 * n + 8 * q + 4 * h) * OS;
-        if constexpr (OUT == TMOE_BF16) *reinterpret_cast<bf4v*>(to) = __builtin_convertvector(v, bf4v);
-        else if constexpr (OUT == TMOE_F16) *reinterpret_cast<hf4v*>(to) = __builtin_convertvector(v, hf4v);
-        else *reinterpret_cast<f4*>(to) = v;
+            for (int n = 0; n < NC; ++n) asm volatile("" : "+a"(acc[m][n0 + n]));
+          }
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f16v& c = acc[m][n0 + n];
+              const f4 v = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+              uint8_t* to = mine + r32 * PITCH + (32 * n + 8 * q + 4 * h) * OS;
+              if constexpr (OUT == TMOE_BF16) *reinterpret_cast<bf4v*>(to) = __builtin_convertvector(v, bf4v);
+              else if constexpr (OUT == TMOE_F16) *reinterpret_cast<hf4v*>(to) = __builtin_convertvector(v, hf4v);
+              else *reinterpret_cast<f4*>(to) = v;
+            }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          constexpr int EPL = 16 / OS, LPR = 32 * NC / EPL, RPI = 64 / LPR;
+          const int c = wcol + 32 * n0 + (lane % LPR) * EPL;
+#pragma unroll
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int r = RPI * i + lane / LPR, row = 32 * (m * S::WT + wt) + r;
+            const i4v v = *reinterpret_cast<const i4v*>(mine + r * PITCH + (lane % LPR) * 16);
+            if (row < t.nrows && c < a.cols)
+              *reinterpret_cast<i4v*>(y + (static_cast<long long>(t.row0 + row) * a.cols + c) * OS) = v;
+          }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
       }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    constexpr int LPR = 32 * NT / EPL, RPI = 64 / LPR;
-    const int c = wcol + (lane % LPR) * EPL;
-#pragma unroll
-    for (int i = 0; i < 32 / RPI; ++i) {
-      const int r = RPI * i + lane / LPR, row = 32 * (wt * MT + m) + r;
-      const i4v v = *reinterpret_cast<const i4v*>(mine + r * PITCH + (lane % LPR) * 16);
-      if (row < t.nrows && c < a.cols)
-        *reinterpret_cast<i4v*>(y + (static_cast<long long>(t.row0 + row) * a.cols + c) * OS) = v;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  }
 }
 
-// The tile list is implied by the offsets: expert e has ceil(rows / TR) row tiles; the rows in front of the first group
-// and behind the last come after all experts. Each workgroup finds its own tile by one scan (two experts a thread).
-// The tiles are dealt to the eight XCDs in contiguous runs (workgroups go to the XCDs in turn), within an expert in
-// groups of four row tiles, so that an XCD's L2 holds what its tiles share.
+constexpr int kMaxTiles = (1 << 24) - 8;         // workgroups of 256 threads: a launch has fewer than 2^32 threads
+
+// The workgroup's tile of linear or grad_x; false: none. The row tiles are implied by the offsets: expert e has ceil(rows / TR)
+// of them; the rows in front of the first group and behind the last come after all experts. Every wavefront looks the tile up
+// by itself: lane l holds the tiles in front of experts 8 l .. 8 l + 7. The work is dealt to the eight XCDs in contiguous runs
+// (workgroups go to the XCDs in turn), within an expert in groups of four row tiles, so that an XCD's L2 holds what its tiles
+// share.
 template <class S>
-__device__ __forceinline__ bool find_tile(const GroupedArgs& a, int col_tiles, int* sh, GroupedTile& t) {
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, E = a.experts;
-  int lo[2], n[2], cnt[2];
+__device__ __forceinline__ bool find_rows_tile(const GroupedArgs& a, int col_tiles, GroupedTile& t) {
+  const int lane = threadIdx.x & 63, E = a.experts;
+  int o[9], first[8], sum = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * tid + i;
-    lo[i] = read_offset(a, min(e, E));
-    const int hi = read_offset(a, min(e + 1, E));
-    n[i] = max(0, hi - lo[i]);
-    cnt[i] = (n[i] + S::TR - 1) / S::TR;
+  for (int i = 0; i < 9; ++i) o[i] = read_offset(a, min(8 * lane + i, E));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    first[i] = sum;
+    sum += (max(0, o[i + 1] - o[i]) + S::TR - 1) / S::TR;
   }
-  int sum = cnt[0] + cnt[1];
+  int up = sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(sum, d, 64);
-    if (lane >= d) sum += o;
+    const int v = __shfl_up(up, d, 64);
+    if (lane >= d) up += v;
   }
-  if (lane == 63) sh[wv] = sum;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    if (p < wv) before += sh[p];
-    all += sh[p];
-  }
-  const int front = uniform(read_offset(a, 0)), back = uniform(read_offset(a, E));
-  const int ft = (front + S::TR - 1) / S::TR, bt = (a.rows - back + S::TR - 1) / S::TR;
-  all = uniform(all);
-  const long long total = static_cast<long long>(all + ft + bt) * col_tiles;
-  const long long per = (total + 7) / 8, j = blockIdx.x / 8;
-  const long long w = (blockIdx.x % 8) * per + j;
-  if (j >= per || w >= total) return false;                  // the same for the whole workgroup
-  const int rt = static_cast<int>(w / col_tiles);
-  int ex = before + sum - cnt[0] - cnt[1];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (rt >= ex && rt < ex + cnt[i]) {
-      sh[4] = 2 * tid + i;
-      sh[5] = lo[i];
-      sh[6] = n[i];
-      sh[7] = ex;
-    }
-    ex += cnt[i];
-  }
-  __syncthreads();
+  const int all = __builtin_amdgcn_readlane(up, 63), front = uniform(o[0]), back = uniform(read_offset(a, E));
+  const int ft = (front + S::TR - 1) / S::TR;
+  // offsets that descend may count rows twice: tiles past the launch's own are left out
+  const int total = min(all + ft + (a.rows - back + S::TR - 1) / S::TR, kMaxTiles / col_tiles) * col_tiles;
+  const int per = (total + 7) / 8, j = static_cast<int>(blockIdx.x / 8), w = static_cast<int>(blockIdx.x % 8) * per + j;
+  if (j >= per || w >= total) return false;      // the same for the whole workgroup
+  const int rt = w / col_tiles;
   t.zero = rt >= all;
   t.k0 = 0;
   t.depth = a.depth;
   if (t.zero) {
-    const int z = rt - all;
+    const int behind = max(0, rt - all - ft), before = min(rt - all, ft);
     t.expert = 0;
-    t.row0 = z < ft ? z * S::TR : back + (z - ft) * S::TR;
-    t.nrows = min(S::TR, (z < ft ? front : a.rows) - t.row0);
-    t.col0 = static_cast<int>(w % col_tiles) * S::TC;
+    t.row0 = rt < all + ft ? before * S::TR : back + behind * S::TR;
+    t.nrows = min(S::TR, rt < all + ft ? front - before * S::TR : a.rows - back - behind * S::TR);
+    t.col0 = w % col_tiles * S::TC;
     return true;
   }
-  const int rows = uniform(sh[6]), first = uniform(sh[7]), tiles = (rows + S::TR - 1) / S::TR;
+  int n = 0, mine = 0;                           // experts that start at or in front of this row tile
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int f = first[i] + up - sum;
+    n += __popcll(__ballot(f <= rt));
+    mine = f <= rt ? f : mine;
+  }
+  const int e = n - 1;                           // the last of them; the ones without rows in front of it start there too
+  const int before = __builtin_amdgcn_readlane(mine, e >> 3);
+  const int lo = uniform(read_offset(a, e)), rows = uniform(read_offset(a, e + 1)) - lo;
+  const int tiles = (rows + S::TR - 1) / S::TR;
   constexpr int G = 4;
-  const int in = static_cast<int>(w - static_cast<long long>(first) * col_tiles);   // within the expert
+  const int in = w - before * col_tiles;         // within the expert
   const int g = in / (G * col_tiles), at = in % (G * col_tiles), rg = min(G, tiles - g * G);
   const int r = g * G + at % rg;
-  t.expert = uniform(sh[4]);
-  t.row0 = uniform(sh[5]) + r * S::TR;
+  t.expert = e;
+  t.row0 = lo + r * S::TR;
   t.nrows = min(S::TR, rows - r * S::TR);
   t.col0 = at / rg * S::TC;
   return true;
 }
 
-template <int KIND, bool CKS, class S, int OUT, bool SCALES4>
-__global__ __launch_bounds__(256, S::kLds > 81920 ? 1 : 2) void k_grouped_rows(GroupedArgs a, int col_tiles) {
-  __shared__ __align__(16) uint8_t lds[S::kLds];
-  GroupedTile t;
-  if (!find_tile<S>(a, col_tiles, reinterpret_cast<int*>(lds), t)) return;
-  __syncthreads();
-  grouped_body<KIND, false, CKS, S, OUT, SCALES4>(a, t, lds);
-}
+// The workgroup's tile of grad_w. Every expert has as many, but their depth is its rows: the experts with more than kPopular
+// times the average come first (`popular` of them at most: that many cannot be more than E / kPopular), their tiles dealt to
+// the XCDs in turn; then the others in contiguous runs, so that an XCD's L2 holds what they share. In the order of the
+// experts, popular ones that come late keep their XCD busy alone (E = 96, K = N = 1024, popularity falling as 1 / rank^1.1,
+// 16384 and 65536 rows: 109 and 241 us, popular ones first 95 and 192).
+constexpr int kPopular = 3;
 
-template <int KIND, class S, int OUT>
-__global__ __launch_bounds__(256, S::kLds > 81920 ? 1 : 2) void k_grouped_grad_w(GroupedArgs a, int row_tiles, int col_tiles) {
-  __shared__ __align__(16) uint8_t lds[S::kLds];
-  const long long per_expert = static_cast<long long>(row_tiles) * col_tiles, total = per_expert * a.experts;
-  const long long per = gridDim.x / 8;
-  const long long w = (blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (w >= total) return;
-  GroupedTile t;
-  t.expert = w / per_expert;
-  const int in = static_cast<int>(w - t.expert * per_expert);
-  const int e = static_cast<int>(t.expert);
+template <class S>
+__device__ __forceinline__ bool find_weight_tile(const GroupedArgs& a, int row_tiles, int col_tiles, int popular, GroupedTile& t) {
+  const int each = row_tiles * col_tiles, total = each * a.experts, per = (total + 7) / 8;
+  const int ahead = (popular * each + 7) / 8 * 8, b = static_cast<int>(blockIdx.x) - ahead;
+  auto is_popular = [&](int n) { return static_cast<long long>(n) * a.experts > static_cast<long long>(kPopular) * a.rows; };
+  int e, in;
+  if (b < 0) {                                   // the same for the whole workgroup
+    const int lane = threadIdx.x & 63, w = static_cast<int>(blockIdx.x);
+    int place = w / each, left = -1, base = 0;   // the popular expert at this place: count down over 64 experts at a time
+    in = w - place * each;
+    unsigned long long set = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int x = min(64 * r + lane, a.experts);   // past the last one: no rows
+      const unsigned long long has = __ballot(is_popular(read_offset(a, min(x + 1, a.experts)) - read_offset(a, x)));
+      const int n = __popcll(has);
+      const bool here = place >= 0 && place < n;
+      set = here ? has : set;
+      base = here ? 64 * r : base;
+      left = here ? place : left;
+      place -= n;                                // negative behind the one that holds it
+    }
+    if (left < 0) return false;
+    const int rank = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(set >> 32),
+                                               __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(set), 0));
+    e = uniform(base + __ffsll(__ballot((set >> lane & 1) && rank == left)) - 1);
+  } else {
+    const int w = b % 8 * per + b / 8;
+    if (w >= total) return false;
+    e = w / each;
+    in = w - e * each;
+  }
+  t.expert = e;
   t.k0 = uniform(read_offset(a, e));
   t.depth = max(0, uniform(read_offset(a, e + 1)) - t.k0);
+  if (b >= 0 && popular > 0 && is_popular(t.depth)) return false;
   t.zero = false;
   constexpr int G = 4;
   const int g = in / (G * col_tiles), at = in % (G * col_tiles), rg = min(G, row_tiles - g * G);
   t.row0 = (g * G + at % rg) * S::TR;
   t.nrows = min(S::TR, a.out_rows - t.row0);
   t.col0 = at / rg * S::TC;
-  grouped_body<KIND, true, true, S, OUT, false>(a, t, lds);
+  return true;
 }
 
-constexpr long long kMaxGroups = (1LL << 24) - 8;   // workgroups of 256 threads: a launch has fewer than 2^32 threads
+template <class S>
+constexpr int kWavesPerSimd = S::kLds > 81920 ? 1 : S::kLds > 40960 ? 2 : 4;
 
-template <int KIND, bool CKS, class S, int OUT, bool SCALES4>
+template <int KIND, bool CKS, class S, int OUT>
+__global__ __launch_bounds__(256, kWavesPerSimd<S>) void k_grouped_rows(GroupedArgs a, int col_tiles) {
+  __shared__ __align__(16) uint8_t lds[S::kLds];
+  GroupedTile t;
+  if (find_rows_tile<S>(a, col_tiles, t)) grouped_body<KIND, false, CKS, S, OUT>(a, t, lds);
+}
+
+template <int KIND, class S, int OUT>
+__global__ __launch_bounds__(256, kWavesPerSimd<S>) void k_grouped_grad_w(GroupedArgs a, int row_tiles, int col_tiles, int popular) {
+  __shared__ __align__(16) uint8_t lds[S::kLds];
+  GroupedTile t;
+  if (find_weight_tile<S>(a, row_tiles, col_tiles, popular, t)) grouped_body<KIND, true, true, S, OUT>(a, t, lds);
+}
+
+template <int KIND, bool CKS, class S, int OUT>
 bool launch_rows(const GroupedArgs& a, hipStream_t s) {
   const int ct = (a.cols + S::TC - 1) / S::TC;
   // every row tile but a group's last is full, the rows in front and behind are two groups more
   const long long tiles = std::min<long long>(a.rows, a.experts + 2 + a.rows / S::TR);
   const long long g = (tiles * ct + 7) / 8 * 8;
-  if (g > kMaxGroups) return false;
-  hipLaunchKernelGGL((k_grouped_rows<KIND, CKS, S, OUT, SCALES4>), dim3(static_cast<unsigned>(g)), dim3(256), 0, s, a, ct);
+  if (g > kMaxTiles) return false;
+  hipLaunchKernelGGL((k_grouped_rows<KIND, CKS, S, OUT>), dim3(static_cast<unsigned>(g)), dim3(256), 0, s, a, ct);
   return true;
 }
 
 template <int KIND, class S, int OUT>
 bool launch_grad_w(const GroupedArgs& a, hipStream_t s) {
   const int rt = (a.out_rows + S::TR - 1) / S::TR, ct = (a.cols + S::TC - 1) / S::TC;
-  const long long g = (static_cast<long long>(rt) * ct * a.experts + 7) / 8 * 8;
-  if (g > kMaxGroups) return false;
-  hipLaunchKernelGGL((k_grouped_grad_w<KIND, S, OUT>), dim3(static_cast<unsigned>(g)), dim3(256), 0, s, a, rt, ct);
+  const int popular = a.rows >= 32LL * a.experts ? (a.experts - 1) / kPopular : 0;
+  const long long each = static_cast<long long>(rt) * ct;
+  const long long g = (each * popular + 7) / 8 * 8 + (each * a.experts + 7) / 8 * 8;
+  if (g > kMaxTiles) return false;
+  hipLaunchKernelGGL((k_grouped_grad_w<KIND, S, OUT>), dim3(static_cast<unsigned>(g)), dim3(256), 0, s, a, rt, ct, popular);
   return true;
 }
 
-template <int KIND> using Few = GTile<KIND, 1, 4, 1, 1, 2>;    // 32 x 128
-template <int KIND> using Mid = GTile<KIND, 2, 2, 2, 2, 2>;    // 128 x 128
-template <int KIND> using Big = GTile<KIND, 2, 2, 4, 4, 2>;    // 256 x 256
+// Row tiles by columns: 32 x 128 (four workgroups a CU) while the weights' bytes count, 128 x 128 (two), 256 x 256 (one).
+template <int KIND, int SCALES = 0> using Few = GTile<KIND, 1, 4, 1, 1, 2, SCALES>;
+template <int KIND, int SCALES = 0> using Mid = GTile<KIND, 2, 2, 2, 2, 2, SCALES>;
+template <int KIND, int SCALES = 0> using Big = GTile<KIND, 2, 2, 4, 4, 2, SCALES>;
+template <int KIND> using Flat = GTile<KIND, 2, 2, 2, 2, 2, 0, 32>;   // 128 x 128, slots of 32 (four)
 
-template <int KIND, bool CKS, int OUT, bool SCALES4>
+// Fewer tiles than this leave CUs idle that smaller tiles would use.
+constexpr long long kFillsChip = 192;
+
+// The tile of linear and grad_x (us; bf16, E = 96, K = N = 1024 unless said; rows an expert on average):
+//   up to 32 rows   32 x 128 (1: 30, 128 x 128 42; 5: 34 and 45; 21: 46 and 52; 32: 51 and 51; 43: 53 and 51)
+//   up to 128       128 x 128 (85: 55, 256 x 256 60; 170: 76 and 70; 683: 207 and 165; MXFP8 170: 45 and 50, 683: 134 and 122,
+//                   so 512 there)
+//   more            256 x 256, where there are enough of them (E = 8, K = 2048, N = 4096, 256 rows: linear, 192 tiles, 56 and
+//                   128 x 128 78; grad_x, 96 tiles, 83 and 77; E = 1, 1024 rows, K = N = 4096, 72 tiles: 72 and 44)
+template <int KIND, bool CKS, int OUT, int SCALES = 0>
 bool launch_rows_by_size(const GroupedArgs& a, hipStream_t s) {
-  if (a.rows <= 16LL * a.experts) return launch_rows<KIND, CKS, Few<KIND>, OUT, SCALES4>(a, s);
-  if constexpr (KIND != kKindMx8 || SCALES4) {   // byte loads of scales leave no registers for 256 x 256
-    if (a.rows >= 1024LL * a.experts) return launch_rows<KIND, CKS, Big<KIND>, OUT, SCALES4>(a, s);
+  const long long E = a.experts, R = a.rows;
+  if (R <= 32 * E) return launch_rows<KIND, CKS, Few<KIND, SCALES>, OUT>(a, s);
+  if constexpr (KIND != kKindMx8 || SCALES > 0) {   // byte loads of scales leave no registers for 256 x 256
+    const long long tiles = (R / 256 + (E + 1) / 2) * ((a.cols + 255) / 256);
+    if (R >= (KIND == kKindMx8 ? 512 : 128) * E && tiles >= kFillsChip) return launch_rows<KIND, CKS, Big<KIND, SCALES>, OUT>(a, s);
   }
-  return launch_rows<KIND, CKS, Mid<KIND>, OUT, SCALES4>(a, s);
+  return launch_rows<KIND, CKS, Mid<KIND, SCALES>, OUT>(a, s);
 }
 
+// The tile of grad_w: 128 x 128 with short slots up to 512 rows an expert (E = 96, K = N = 1024: 1 row 31, 256 x 256 45; 21: 36
+// and 47; 170: 84 and 79; E = 8, 256 rows, K = 2048, N = 4096: 52 and 59), 256 x 256 beyond (683: 185 and 160; E = 8, 2048 rows,
+// K = 2048, N = 4096: 293 and 234), where there are enough of them.
 template <int KIND, int OUT>
 bool launch_16bit(const GroupedArgs& a, int op, hipStream_t s) {
-  if (op == kGroupedLinear) return launch_rows_by_size<KIND, false, OUT, false>(a, s);
-  if (op == kGroupedGradX) return launch_rows_by_size<KIND, true, OUT, false>(a, s);
-  if (a.rows < 1024LL * a.experts) return launch_grad_w<KIND, Mid<KIND>, OUT>(a, s);
-  return launch_grad_w<KIND, Big<KIND>, OUT>(a, s);
+  if (op == kGroupedLinear) return launch_rows_by_size<KIND, false, OUT>(a, s);
+  if (op == kGroupedGradX) return launch_rows_by_size<KIND, true, OUT>(a, s);
+  const long long tiles = static_cast<long long>((a.out_rows + 255) / 256) * ((a.cols + 255) / 256) * a.experts;
+  if (a.rows >= 512LL * a.experts && tiles >= kFillsChip) return launch_grad_w<KIND, Big<KIND>, OUT>(a, s);
+  return launch_grad_w<KIND, Flat<KIND>, OUT>(a, s);
 }
 
 }  // namespace
