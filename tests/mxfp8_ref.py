@@ -66,14 +66,14 @@ def norm_grad(h, g, eps, dy, dh):
 
 def norm_grad_bounds(h, g, eps, dy, dh, half_x, tiny_x, half_g, tiny_g):
     """u = h r is off by NORM_R + 1 units, c by those, the products and 38 additions of |d u|; dx by c's and u's share, its own
-    four roundings and r's. dg sums dy u over the rows: at most 1 + T / 1024 of them in a lane, then n / 16 + 16 partial
-    sums with n <= 4096."""
+    four roundings and r's. dg sums dy u over the rows: at most 1 + T / 256 of them in a lane, 8 across a
+    workgroup's rows, then n / 64 + 6 partial sums with n <= 2048."""
     dx, dg = norm_grad(h, g, eps, dy, dh)
     _, u, r = norm(h, g, eps)
     d = dy * g
     a = np.abs(d * u).mean(-1, keepdims=True)
     ex = r * (np.abs(u) * a * (2 * NORM_R + 50) + np.abs(d) * (NORM_R + 6)) * U + (0 if dh is None else np.abs(dh) * U)
-    eg = np.abs(dy * u).sum(0) * (NORM_R + 2 + 2 + len(h) / 1024 + 4096 / 16 + 16) * U
+    eg = np.abs(dy * u).sum(0) * (NORM_R + 2 + 1 + len(h) / 256 + 8 + 2048 / 64 + 6) * U
     return half_x * np.abs(dx) + 1.01 * ex + tiny_x, half_g * np.abs(dg) + 1.01 * eg + tiny_g
 
 

@@ -36,18 +36,30 @@ struct F16 {
   static __device__ __forceinline__ uint16_t put(float v) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v)); }
 };
 
-// V neighbouring values of a row of H from element `at`; zeros past the end.
-template <class D, int V>
-__device__ __forceinline__ void load_vec(const typename D::T* row, int at, int H, float (&v)[V]) {
-  typename D::T raw[V];
+template <class T, int V>
+struct Raw {
+  T v[V];
+};
+
+// V neighbouring values of a row of H from element `at`, as they are; zeros past the end.
+template <class T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T* row, int at, int H) {
+  Raw<T, V> r;
   if (at + V <= H) {
-    __builtin_memcpy(raw, row + at, sizeof(raw));
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = D::get(raw[i]);
+    __builtin_memcpy(r.v, row + at, sizeof(r.v));
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = at + i < H ? D::get(row[at + i]) : 0.0f;
+    for (int i = 0; i < V; ++i) r.v[i] = at + i < H ? row[at + i] : T{};
   }
+  return r;
+}
+
+// The same as fp32.
+template <class D, int V>
+__device__ __forceinline__ void load_vec(const typename D::T* row, int at, int H, float (&v)[V]) {
+  const Raw<typename D::T, V> r = load_raw<typename D::T, V>(row, at, H);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = D::get(r.v[i]);
 }
 template <class D, int V>
 __device__ __forceinline__ void store_vec(typename D::T* row, int at, int H, const float (&v)[V]) {
@@ -155,69 +167,116 @@ __global__ void k_rms_norm(NormArgs a) {
   }
 }
 
-// One pass over the rows, workgroup g of a.groups every groups-th batch of rows; dweight's sums over its rows stay in
-// registers and leave as one row of partial sums.
-template <class D, class W, int NV, bool WIDE>
-__global__ void k_rms_norm_grad(NormGradArgs a) {
+// One pass over the rows, workgroup g of a.groups every groups-th batch of rows, the next row's loads ahead of this one's sum;
+// dweight's sums over its rows stay in registers, are joined over the workgroup's rows and leave as one row of partial sums.
+template <class D, class W, int NV, bool WIDE, int WAVES = NV == 1 ? 5 : 4>
+__global__ __launch_bounds__(WIDE ? 1024 : 512, WAVES) void k_rms_norm_grad(NormGradArgs a) {
   constexpr int V = D::V;
+  typedef typename D::T T;
   __shared__ float sh[2][16];
   const int H = a.hidden, tid = threadIdx.x, threads = blockDim.x, rows = blockDim.y;
-  const typename W::T* w = static_cast<const typename W::T*>(a.weight);
-  float dg[NV][V] = {};
-  int turn = 0;
-  for (long long t = blockIdx.x * rows + threadIdx.y; t < a.tokens; t += static_cast<long long>(a.groups) * rows) {
+  float g[NV][V], dg[NV][V] = {};
+#pragma unroll
+  for (int j = 0; j < NV; ++j) load_vec<W, V>(static_cast<const typename W::T*>(a.weight), (j * threads + tid) * V, H, g[j]);
+  struct Row {
+    Raw<T, V> h[NV], dy[NV], dh[NV];
+    float r;
+  };
+  auto load = [&](long long t, Row& o) {
+    const T* hp = static_cast<const T*>(a.h) + t * a.h_stride;
     const long long row = t * H;
-    const typename D::T* hp = static_cast<const typename D::T*>(a.h) + t * a.h_stride;
-    float h[NV][V], d[NV][V];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load_vec<D, V>(hp, (j * threads + tid) * V, H, h[j]);
-      load_vec<D, V>(static_cast<const typename D::T*>(a.dy) + row, (j * threads + tid) * V, H, d[j]);
+      const int at = (j * threads + tid) * V;
+      o.h[j] = load_raw<T, V>(hp, at, H);
+      o.dy[j] = load_raw<T, V>(static_cast<const T*>(a.dy) + row, at, H);
+      if (a.dh) o.dh[j] = load_raw<T, V>(static_cast<const T*>(a.dh) + row, at, H);
     }
-    const float r = a.rstd[t];
-    float c = 0.0f;
+    o.r = a.rstd[t];
+  };
+  const long long step = static_cast<long long>(a.groups) * rows;
+  int turn = 0;
+  Row now, next;
+  long long t = static_cast<long long>(blockIdx.x) * rows + threadIdx.y;
+  if (t < a.tokens) load(t, now);
+  for (; t < a.tokens; t += step) {              // WIDE: the same rows for the whole workgroup
+    if (t + step < a.tokens) load(t + step, next);
+    float u[NV][V], d[NV][V], c = 0.0f;
+    const float r = now.r;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float g[V];
-      load_vec<W, V>(w, (j * threads + tid) * V, H, g);
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        h[j][i] *= r;                            // the row's unit values
-        dg[j][i] = fmaf(d[j][i], h[j][i], dg[j][i]);
-        d[j][i] *= g[i];
-        c = fmaf(d[j][i], h[j][i], c);
+        u[j][i] = D::get(now.h[j].v[i]) * r;     // the row's unit values
+        const float dy = D::get(now.dy[j].v[i]);
+        dg[j][i] = fmaf(dy, u[j][i], dg[j][i]);
+        d[j][i] = dy * g[j][i];
+        c = fmaf(d[j][i], u[j][i], c);
       }
-    }
     c = row_sum<WIDE>(c, sh[turn]) / static_cast<float>(H);
     turn ^= 1;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int at = (j * threads + tid) * V;
-      float o[V] = {};
-      if (a.dh) load_vec<D, V>(static_cast<const typename D::T*>(a.dh) + row, at, H, o);
+      float o[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = fmaf(r, fmaf(-h[j][i], c, d[j][i]), o[i]);
-      store_vec<D, V>(static_cast<typename D::T*>(a.dx) + row, at, H, o);
+      for (int i = 0; i < V; ++i) o[i] = fmaf(r, fmaf(-u[j][i], c, d[j][i]), a.dh ? D::get(now.dh[j].v[i]) : 0.0f);
+      store_vec<D, V>(static_cast<T*>(a.dx) + t * H, (j * threads + tid) * V, H, o);
     }
+    now = next;
   }
-  float* part = a.part + static_cast<long long>(blockIdx.x * rows + threadIdx.y) * H;
+  float* part = a.part + static_cast<long long>(blockIdx.x) * H;
+  if constexpr (!WIDE) {                         // the rows' wavefronts add up in order
+    __shared__ float sum[NV * V][64];
+    for (int p = 0; p < rows; ++p) {
+      if (threadIdx.y == p) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if (p > 0) dg[j][i] += sum[j * V + i][tid];
+            sum[j * V + i][tid] = dg[j][i];
+          }
+      }
+      __syncthreads();
+    }
+    if (threadIdx.y != rows - 1) return;
+  }
 #pragma unroll
   for (int j = 0; j < NV; ++j) store_vec<F32, V>(part, (j * threads + tid) * V, H, dg[j]);
 }
 
-// dweight: 64 columns a workgroup, its 16 wavefronts every 16th partial row, joined in a fixed order.
+// dweight: 16 columns a workgroup, 64 threads a column with every 64th partial row, joined in a fixed order.
 template <class W>
 __global__ __launch_bounds__(1024) void k_rms_norm_dweight(const float* part, int n, int H, void* dweight) {
-  __shared__ float sh[16][64];
-  const int c = blockIdx.x * 64 + threadIdx.x, at = min(c, H - 1);
+  __shared__ float sh[64][17];
+  const int c = blockIdx.x * 16 + threadIdx.x, at = min(c, H - 1);
   float s = 0.0f;
-  for (int p = threadIdx.y; p < n; p += 16) s += part[static_cast<long long>(p) * H + at];
+#pragma unroll 8
+  for (int p = threadIdx.y; p < n; p += 64) s += part[static_cast<long long>(p) * H + at];
   sh[threadIdx.y][threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.y == 0 && c < H) {
-    for (int p = 1; p < 16; ++p) s += sh[p][threadIdx.x];
-    static_cast<typename W::T*>(dweight)[c] = W::put(s);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    __syncthreads();
+    if (static_cast<int>(threadIdx.y) < d) sh[threadIdx.y][threadIdx.x] += sh[threadIdx.y + d][threadIdx.x];
   }
+  if (threadIdx.y == 0 && c < H) static_cast<typename W::T*>(dweight)[c] = W::put(sh[0][threadIdx.x]);
+}
+
+// The gradient's: one vector a lane as far as a workgroup goes (it holds five of them at a time), eight rows of up to 64
+// vectors a workgroup.
+NormShape grad_shape(int hidden, int dtype) {
+  const int v = dtype == TMOE_F32 ? 4 : 8, vecs = (hidden + v - 1) / v;
+  NormShape n;
+  n.nv = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
+  n.threads = ((vecs + n.nv - 1) / n.nv + 63) / 64 * 64;
+  n.rows = n.threads == 64 ? 8 : 1;
+  return n;
+}
+
+// Wavefronts a SIMD: with 80 registers instead of 96 a CU holds three rows of six to eight wavefronts, not two (16384 rows of
+// 4096 bf16: 111 us instead of 119; the others lose by it: 8192 rows of 8192 138 and 120, 2048 fp32 values a row 108 and 101).
+int grad_waves(const NormShape& n, int dtype) {
+  return n.nv > 1 ? 4 : dtype != TMOE_F32 && n.threads > 320 && n.threads <= 512 && n.rows == 1 ? 6 : 5;
 }
 
 template <class D, class W, bool MX>
@@ -229,28 +288,29 @@ void launch_norm(const NormArgs& a, int dtype, hipStream_t s) {
     else if (n.nv == 2) hipLaunchKernelGGL((k_rms_norm<D, W, 2, false, MX>), g, b, 0, s, a);
     else hipLaunchKernelGGL((k_rms_norm<D, W, 4, false, MX>), g, b, 0, s, a);
   } else {
-    if (n.nv == 1) hipLaunchKernelGGL((k_rms_norm<D, W, 1, true, MX>), g, b, 0, s, a);
-    else if (n.nv == 2) hipLaunchKernelGGL((k_rms_norm<D, W, 2, true, MX>), g, b, 0, s, a);
-    else hipLaunchKernelGGL((k_rms_norm<D, W, 4, true, MX>), g, b, 0, s, a);
+    if (n.nv == 2) hipLaunchKernelGGL((k_rms_norm<D, W, 2, true, MX>), g, b, 0, s, a);
+    else if constexpr (D::V == 4) hipLaunchKernelGGL((k_rms_norm<D, W, 4, true, MX>), g, b, 0, s, a);   // fp32 rows beyond 8192
   }
 }
 
 template <class D, class W>
 void launch_grad(const NormGradArgs& a, int dtype, hipStream_t s) {
-  const NormShape n = norm_shape(a.hidden, dtype);
+  const NormShape n = grad_shape(a.hidden, dtype);
   const dim3 g(a.groups), b(n.threads, n.rows);
   if (a.groups == 0) {
   } else if (n.threads == 64) {
-    if (n.nv == 1) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, false>), g, b, 0, s, a);
-    else if (n.nv == 2) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 2, false>), g, b, 0, s, a);
-    else hipLaunchKernelGGL((k_rms_norm_grad<D, W, 4, false>), g, b, 0, s, a);
+    hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, false>), g, b, 0, s, a);
+  } else if (grad_waves(n, dtype) == 6) {
+    if constexpr (D::V == 8) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, true, 6>), g, b, 0, s, a);
+  } else if (n.nv == 1) {
+    hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, true>), g, b, 0, s, a);
+  } else if (n.nv == 2) {
+    hipLaunchKernelGGL((k_rms_norm_grad<D, W, 2, true>), g, b, 0, s, a);
   } else {
-    if (n.nv == 1) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, true>), g, b, 0, s, a);
-    else if (n.nv == 2) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 2, true>), g, b, 0, s, a);
-    else hipLaunchKernelGGL((k_rms_norm_grad<D, W, 4, true>), g, b, 0, s, a);
+    if constexpr (D::V == 4) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 4, true>), g, b, 0, s, a);   // fp32 rows beyond 8192
   }
-  hipLaunchKernelGGL((k_rms_norm_dweight<W>), dim3((a.hidden + 63) / 64), dim3(64, 16), 0, s, a.part, a.groups * n.rows,
-                     a.hidden, a.dweight);
+  hipLaunchKernelGGL((k_rms_norm_dweight<W>), dim3((a.hidden + 15) / 16), dim3(16, 64), 0, s, a.part, a.groups, a.hidden,
+                     a.dweight);
 }
 
 }  // namespace
@@ -270,9 +330,13 @@ NormShape norm_shape(int hidden, int dtype) {
   return n;
 }
 
+// As many workgroups as the chip holds at once (more would come in a second round), but not so many that their partial sums
+// count beside the rows (2047 rows of 2560 fp16: 1024 groups 27 us, 511 19).
 int norm_grad_groups(int tokens, int hidden, int dtype) {
-  const NormShape n = norm_shape(hidden, dtype);
-  return std::max(1, std::min((tokens + n.rows - 1) / n.rows, 1024));
+  const NormShape n = grad_shape(hidden, dtype);
+  const int waves = n.threads * n.rows / 64, batches = (tokens + n.rows - 1) / n.rows;
+  const int resident = 256 * std::clamp(4 * grad_waves(n, dtype) / waves, 1, 8);
+  return std::max(1, std::min({batches, resident, std::max(256, batches / 4)}));
 }
 
 void launch_rms_norm(const NormArgs& a, int dtype, bool weight_f32, bool mxfp8, hipStream_t s) {

@@ -71,8 +71,7 @@ tmoe_status norm(const tmoe_norm_config* c, const void* x, int64_t x_stride, con
 
 size_t grad_scratch(const tmoe_norm_config* c, int32_t T) {
   if (T == 0) return 0;
-  const int rows = norm_grad_groups(T, c->hidden, c->dtype) * norm_shape(c->hidden, c->dtype).rows;
-  return 4ull * rows * c->hidden;
+  return 4ull * norm_grad_groups(T, c->hidden, c->dtype) * c->hidden;
 }
 
 tmoe_status check_blocks(const void* x, int32_t dtype, int64_t rows, int32_t cols, const void* codes,

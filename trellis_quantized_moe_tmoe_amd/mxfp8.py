@@ -35,7 +35,7 @@ def quantize(x: torch.Tensor):
     if not x.is_cuda:
         _same_device([("x", x)])
     dev = x.device
-    codes = torch.empty(x.shape, dtype=torch.uint8, device=dev)
+    codes = torch.empty_like(x, dtype=torch.uint8)
     scales = torch.empty((*x.shape[:-1], K // 32), dtype=torch.uint8, device=dev)
     _launch(dev.index, lib.tmoe_mxfp8_quantize, "tmoe_mxfp8_quantize", x.data_ptr(), _DTYPES[x.dtype], x.numel() // K, K,
             codes.data_ptr(), scales.data_ptr())
@@ -66,7 +66,7 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float32) -
     if not _one_gpu(codes, scales):
         _same_device([("codes", codes), ("scales", scales)])
     dev = codes.device
-    x = torch.empty(codes.shape, dtype=dtype, device=dev)
+    x = torch.empty_like(codes, dtype=dtype)
     _launch(dev.index, lib.tmoe_mxfp8_dequantize, "tmoe_mxfp8_dequantize", codes.data_ptr(), scales.data_ptr(),
             x.numel() // K, K, _DTYPES[dtype], x.data_ptr())
     return x

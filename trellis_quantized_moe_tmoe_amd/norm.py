@@ -17,6 +17,7 @@ from . import native
 from .layer import _fits, _in_forward_mode, _int32, _launch, _no_gradient, _one_gpu, _refuse_duals, _require, _same_device
 from .native import check, lib
 
+_ROWS = torch.contiguous_format                  # of outputs: empty_like takes half the time of empty with a shape
 _DTYPES = {torch.float32: native.F32, torch.bfloat16: native.BF16, torch.float16: native.F16}
 
 
@@ -72,11 +73,11 @@ def _inputs(x, weight, residual, eps):
 def _rms_norm(x, weight, residual, eps):
     cfg, stride, res_stride = _inputs(x, weight, residual, eps)
     T, dev = x.shape[0], x.device
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = torch.empty_like(x, memory_format=_ROWS)
     rstd = torch.empty(T, dtype=torch.float32, device=dev)
     h, ph, pr = x, None, None
     if residual is not None:
-        h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        h = torch.empty_like(x, memory_format=_ROWS)
         ph, pr = h.data_ptr(), residual.data_ptr()
     _launch(dev.index, lib.tmoe_rms_norm, "tmoe_rms_norm", cfg, x.data_ptr(), stride, pr, res_stride, weight.data_ptr(), T,
             y.data_ptr(), ph, rstd.data_ptr())
@@ -104,8 +105,8 @@ def backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torc
         tensors.append(dh)
     if not _one_gpu(h, *tensors):
         _same_device([("h", h)] + list(zip(("weight", "rstd", "dy", "dh"), tensors)))
-    dx = torch.empty(shape, dtype=dtype, device=dev)
-    dweight = torch.empty(weight.shape, dtype=weight.dtype, device=dev)
+    dx = torch.empty_like(h, memory_format=_ROWS)
+    dweight = torch.empty_like(weight)
     need = _scratch_bytes(cfg, T)
     scratch = torch.empty(need, dtype=torch.uint8, device=dev)
     _launch(dev.index, lib.tmoe_rms_norm_backward, "tmoe_rms_norm_backward", cfg, h.data_ptr(), stride, weight.data_ptr(),
@@ -152,11 +153,11 @@ def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     (T, H), dev = x.shape, x.device
     if H % 32:
         raise ValueError(f"x: rows of {H} values, expected a multiple of 32")
-    codes = torch.empty((T, H), dtype=torch.uint8, device=dev)
+    codes = torch.empty_like(x, dtype=torch.uint8, memory_format=_ROWS)
     scales = torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
     h, ph, pr = x, None, None
     if residual is not None:
-        h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        h = torch.empty_like(x, memory_format=_ROWS)
         ph, pr = h.data_ptr(), residual.data_ptr()
     _launch(dev.index, lib.tmoe_rms_norm_mxfp8, "tmoe_rms_norm_mxfp8", cfg, x.data_ptr(), stride, pr, res_stride,
             weight.data_ptr(), T, codes.data_ptr(), scales.data_ptr(), ph)
