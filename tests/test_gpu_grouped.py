@@ -293,7 +293,7 @@ def test_mxfp8(sizes, N, front, back, K):
 
 def test_mxfp8_256_x_256_tiles():
     off, R = _offsets([1100, 0, 700], 3, 9)
-    for K, N in ((512, 10008), (896, 8200), (2304, 8200)):
+    for K, N in ((4096, 8200), (4224, 7944), (512, 10008)):
         gen = torch.Generator(device="cuda").manual_seed(K)
         (xq, xs), (wq, ws) = (_mx().quantize(torch.randn(*s, generator=gen, device="cuda")) for s in ((R, K), (3, N, K)))
         y = _mx().grouped_linear(xq, xs, wq, ws, torch.from_numpy(off).cuda(), torch.float32)
@@ -308,7 +308,7 @@ def test_mxfp8_256_x_256_tiles():
         assert torch.all(y[:3] == 0) and torch.all(y[-9:] == 0)
 
 
-@pytest.mark.parametrize("sizes,K,N", [([1, 0, 40], 32, 24), ([30, 2, 70], 96, 136), ([500], 1088, 264), ([2000, 9], 640, 72), ([1040], 640, 10008)])
+@pytest.mark.parametrize("sizes,K,N", [([1, 0, 40], 32, 24), ([30, 2, 70], 96, 136), ([500], 1088, 264), ([2000, 9], 640, 72), ([1040], 640, 10008), ([540], 4224, 16392)])
 def test_mxfp8_products_of_one_size_are_exact(sizes, K, N):
     """Values 1, 2 and 3 times a power of two by blocks: nothing is cut and every sum fits fp32, so every product counts."""
     off, R = _offsets(sizes)

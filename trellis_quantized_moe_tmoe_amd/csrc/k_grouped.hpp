@@ -406,48 +406,49 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
     }
   }
 
-      // Results leave through the wavefront's own part of LDS, 32 rows and 128 bytes of them at a time, so that a store covers
-      // whole lines.
-      constexpr int OS = OUT == TMOE_F32 ? 4 : 2, NC = NT == 1 || OUT == TMOE_F32 ? 1 : 2, PITCH = 32 * NC * OS + 16;
-      static_assert(4 * 32 * PITCH <= S::kLds, "four wavefronts' rows fit the ring");
-      const int wcol = t.col0 + 32 * NT * wc;
-      uint8_t* y = static_cast<uint8_t*>(a.y);
-      if constexpr (RKS) y += t.expert * a.out_rows * a.cols * OS;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // copies past the end land before the ring is used again
-      __syncthreads();
-      uint8_t* mine = lds + wv * 32 * PITCH;
+      // Results leave through the wavefront's own part of LDS, MB by NC fragments at a time, so that a store covers whole lines of
+  // a row.
+  constexpr int OS = OUT == TMOE_F32 ? 4 : 2, EPL = 16 / OS;
+  constexpr int NC = 4 * 32 * (32 * NT * OS + 16) > S::kLds ? NT / 2 : NT, PITCH = 32 * NC * OS + 16;
+  constexpr int MB = MT == 1 || 4 * 2 * 32 * PITCH > S::kLds ? 1 : 2;
+  static_assert(4 * MB * 32 * PITCH <= S::kLds && MT % MB == 0 && NT % NC == 0, "four wavefronts' rows fit the ring");
+  const int wcol = t.col0 + 32 * NT * wc;
+  uint8_t* y = static_cast<uint8_t*>(a.y);
+  if constexpr (RKS) y += t.expert * a.out_rows * a.cols * OS;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // copies past the end land before the ring is used again
+  __syncthreads();
+  uint8_t* mine = lds + wv * MB * 32 * PITCH;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+  for (int m0 = 0; m0 < MT; m0 += MB)
 #pragma unroll
-        for (int n0 = 0; n0 < NT; n0 += NC) {
-          if constexpr (MM == 16) {                // 256 sums a lane: they stay where they are until their turn, or they spill
+    for (int n0 = 0; n0 < NT; n0 += NC) {
 #pragma unroll
-            for (int n = 0; n < NC; ++n) asm volatile("" : "+a"(acc[m][n0 + n]));
+      for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          f16v& c = acc[m0 + b][n0 + n];
+          if constexpr (MM == 16) asm volatile("" : "+a"(c));   // 256 sums a lane stay where they are until their turn, or spill
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f4 v = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+            uint8_t* to = mine + (32 * b + r32) * PITCH + (32 * n + 8 * q + 4 * h) * OS;
+            if constexpr (OUT == TMOE_BF16) *reinterpret_cast<bf4v*>(to) = __builtin_convertvector(v, bf4v);
+            else if constexpr (OUT == TMOE_F16) *reinterpret_cast<hf4v*>(to) = __builtin_convertvector(v, hf4v);
+            else *reinterpret_cast<f4*>(to) = v;
           }
-#pragma unroll
-          for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const f16v& c = acc[m][n0 + n];
-              const f4 v = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-              uint8_t* to = mine + r32 * PITCH + (32 * n + 8 * q + 4 * h) * OS;
-              if constexpr (OUT == TMOE_BF16) *reinterpret_cast<bf4v*>(to) = __builtin_convertvector(v, bf4v);
-              else if constexpr (OUT == TMOE_F16) *reinterpret_cast<hf4v*>(to) = __builtin_convertvector(v, hf4v);
-              else *reinterpret_cast<f4*>(to) = v;
-            }
-          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-          constexpr int EPL = 16 / OS, LPR = 32 * NC / EPL, RPI = 64 / LPR;
-          const int c = wcol + 32 * n0 + (lane % LPR) * EPL;
-#pragma unroll
-          for (int i = 0; i < 32 / RPI; ++i) {
-            const int r = RPI * i + lane / LPR, row = 32 * (m * S::WT + wt) + r;
-            const i4v v = *reinterpret_cast<const i4v*>(mine + r * PITCH + (lane % LPR) * 16);
-            if (row < t.nrows && c < a.cols)
-              *reinterpret_cast<i4v*>(y + (static_cast<long long>(t.row0 + row) * a.cols + c) * OS) = v;
-          }
-          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      constexpr int LPR = 32 * NC / EPL, RPI = 64 / LPR;   // lanes a row, rows a store
+      const int c = wcol + 32 * n0 + (lane % LPR) * EPL;
+#pragma unroll
+      for (int i = 0; i < MB * 32 / RPI; ++i) {
+        const int r = RPI * i + lane / LPR, row = 32 * ((m0 + r / 32) * S::WT + wt) + r % 32;
+        const i4v v = *reinterpret_cast<const i4v*>(mine + r * PITCH + (lane % LPR) * 16);
+        if (row < t.nrows && c < a.cols)
+          *reinterpret_cast<i4v*>(y + (static_cast<long long>(t.row0 + row) * a.cols + c) * OS) = v;
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
 }
 
 constexpr int kMaxTiles = (1 << 24) - 8;         // workgroups of 256 threads: a launch has fewer than 2^32 threads
@@ -468,13 +469,15 @@ __device__ __forceinline__ bool find_rows_tile(const GroupedArgs& a, int col_til
     first[i] = sum;
     sum += (max(0, o[i + 1] - o[i]) + S::TR - 1) / S::TR;
   }
+  // the lanes' prefix sums by DPP: within 16 lanes, then across them
   int up = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(up, d, 64);
-    if (lane >= d) up += v;
-  }
-  const int all = __builtin_amdgcn_readlane(up, 63), front = uniform(o[0]), back = uniform(read_offset(a, E));
+  up += __builtin_amdgcn_update_dpp(0, up, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
+  up += __builtin_amdgcn_update_dpp(0, up, 0x112, 0xF, 0xF, false);
+  up += __builtin_amdgcn_update_dpp(0, up, 0x114, 0xF, 0xF, false);
+  up += __builtin_amdgcn_update_dpp(0, up, 0x118, 0xF, 0xF, false);
+  up += __builtin_amdgcn_update_dpp(0, up, 0x142, 0xA, 0xF, false);   // row_bcast 15 to rows 1 and 3, 31 to rows 2 and 3
+  up += __builtin_amdgcn_update_dpp(0, up, 0x143, 0xC, 0xF, false);
+  const int all = __builtin_amdgcn_readlane(up, 63), front = uniform(o[0]), back = __builtin_amdgcn_readlane(o[8], 63);
   const int ft = (front + S::TR - 1) / S::TR;
   // offsets that descend may count rows twice: tiles past the launch's own are left out
   const int total = min(all + ft + (a.rows - back + S::TR - 1) / S::TR, kMaxTiles / col_tiles) * col_tiles;
@@ -492,16 +495,19 @@ __device__ __forceinline__ bool find_rows_tile(const GroupedArgs& a, int col_til
     t.col0 = w % col_tiles * S::TC;
     return true;
   }
-  int n = 0, mine = 0;                           // experts that start at or in front of this row tile
+  // experts that start at or in front of this row tile; of this lane's, the last one's first tile, first row and end
+  int n = 0, mine = 0, mlo = 0, mhi = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int f = first[i] + up - sum;
     n += __popcll(__ballot(f <= rt));
     mine = f <= rt ? f : mine;
+    mlo = f <= rt ? o[i] : mlo;
+    mhi = f <= rt ? o[i + 1] : mhi;
   }
-  const int e = n - 1;                           // the last of them; the ones without rows in front of it start there too
-  const int before = __builtin_amdgcn_readlane(mine, e >> 3);
-  const int lo = uniform(read_offset(a, e)), rows = uniform(read_offset(a, e + 1)) - lo;
+  const int e = n - 1;                           // the last of all; the ones without rows in front of it start there too
+  const int before = __builtin_amdgcn_readlane(mine, e >> 3), lo = __builtin_amdgcn_readlane(mlo, e >> 3);
+  const int rows = __builtin_amdgcn_readlane(mhi, e >> 3) - lo;
   const int tiles = (rows + S::TR - 1) / S::TR;
   constexpr int G = 4;
   const int in = w - before * col_tiles;         // within the expert
@@ -573,7 +579,17 @@ template <int KIND, bool CKS, class S, int OUT>
 __global__ __launch_bounds__(256, kWavesPerSimd<S>) void k_grouped_rows(GroupedArgs a, int col_tiles) {
   __shared__ __align__(16) uint8_t lds[S::kLds];
   GroupedTile t;
-  if (find_rows_tile<S>(a, col_tiles, t)) grouped_body<KIND, false, CKS, S, OUT>(a, t, lds);
+  if (!find_rows_tile<S>(a, col_tiles, t)) return;
+  if constexpr (S::MT == 4 && KIND != kKindMx8) {
+    // A group's last tile, of at most half the rows, with half the fragments (E = 96, K = N = 1024, 16384 rows with uneven
+    // popularity: linear 72 -> 69.5 us, grad_x 72 -> 65.5; MXFP8 leaves single fragments out).
+    using Half = GTile<KIND, S::WT, S::WC, 2, S::NT, S::SLOTS>;
+    if (t.nrows <= Half::TR) {
+      grouped_body<KIND, false, CKS, Half, OUT>(a, t, lds);
+      return;
+    }
+  }
+  grouped_body<KIND, false, CKS, S, OUT>(a, t, lds);
 }
 
 template <int KIND, class S, int OUT>
@@ -616,17 +632,19 @@ constexpr long long kFillsChip = 192;
 
 // The tile of linear and grad_x (us; bf16, E = 96, K = N = 1024 unless said; rows an expert on average):
 //   up to 32 rows   32 x 128 (1: 30, 128 x 128 42; 5: 34 and 45; 21: 46 and 52; 32: 51 and 51; 43: 53 and 51)
-//   up to 128       128 x 128 (85: 55, 256 x 256 60; 170: 76 and 70; 683: 207 and 165; MXFP8 170: 45 and 50, 683: 134 and 122,
-//                   so 512 there)
+//   up to 128       128 x 128 (85: 55, 256 x 256 60; 170: 76 and 70; 683: 207 and 164)
 //   more            256 x 256, where there are enough of them (E = 8, K = 2048, N = 4096, 256 rows: linear, 192 tiles, 56 and
 //                   128 x 128 78; grad_x, 96 tiles, 83 and 77; E = 1, 1024 rows, K = N = 4096, 72 tiles: 72 and 44)
+// MXFP8 has half the slots for the same depth, so what a tile costs before and behind them counts more: 256 x 256 from a depth of
+// 4096 on (E = 1, 4096 rows, K = N = 4096: 65 and 76; depth 2048, E = 8, N = 4096, 2048 rows: 190 and 184; 1024, E = 96, 683
+// rows: 145 and 134).
 template <int KIND, bool CKS, int OUT, int SCALES = 0>
 bool launch_rows_by_size(const GroupedArgs& a, hipStream_t s) {
   const long long E = a.experts, R = a.rows;
   if (R <= 32 * E) return launch_rows<KIND, CKS, Few<KIND, SCALES>, OUT>(a, s);
   if constexpr (KIND != kKindMx8 || SCALES > 0) {   // byte loads of scales leave no registers for 256 x 256
     const long long tiles = (R / 256 + (E + 1) / 2) * ((a.cols + 255) / 256);
-    if (R >= (KIND == kKindMx8 ? 512 : 128) * E && tiles >= kFillsChip) return launch_rows<KIND, CKS, Big<KIND, SCALES>, OUT>(a, s);
+    if (R >= 128 * E && tiles >= kFillsChip && (KIND != kKindMx8 || a.depth >= 4096)) return launch_rows<KIND, CKS, Big<KIND, SCALES>, OUT>(a, s);
   }
   return launch_rows<KIND, CKS, Mid<KIND, SCALES>, OUT>(a, s);
 }
