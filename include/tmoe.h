@@ -355,8 +355,8 @@ tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t plan, const void *x_bf16, const
  * and from dy and the gradient dh that reaches h from elsewhere (null: none)
  *   dx = dh + r (g dy - h r^2 mean(g dy h))       the gradient of x and of the residual alike
  *   dg = sum over rows of dy h r
- * Sums are held in fp32; every output is rounded once. A row whose squares sum past fp32's largest value gives y = 0,
- * one with an infinity or a NaN gives NaN. Outputs must not overlap inputs. */
+ * Sums are held in fp32; every output is rounded once. A row whose squares sum past fp32's largest value gives y = 0
+ * (and NaN where it holds an infinity), one with a NaN gives NaN. Outputs must not overlap inputs. */
 typedef struct {
   int32_t hidden;              /* H: 1..16384; MXFP8 output: a multiple of 32                    */
   int32_t dtype;               /* of x, residual, h, y and their gradients: TMOE_F32, BF16, F16  */

@@ -202,6 +202,27 @@ def test_rows_beyond_32_bits_of_bytes(E):
     assert torch.all(dx[: R - last].view(torch.int16).amax() == 0)
 
 
+def test_weights_beyond_32_bits_of_bytes():
+    """w and dw of more than 4 GiB: only the last expert has rows, only its weights are read."""
+    g = _g()
+    E, N, K, R = 270, 2048, 4096, 9
+    w = torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w[-1] = (torch.randn(N, K, generator=gen, device="cuda") / 64).bfloat16()
+    w[:-1].fill_(float("nan"))
+    x = torch.randn(R, K, generator=gen, device="cuda").bfloat16()
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[-1] = R
+    y = g.linear(x, w, off)
+    _close(y, _np(x.double() @ w[-1].double().t()), _np(x.double().abs() @ w[-1].double().abs().t()), K)
+    dx = g.grad_x(y, w, off)
+    _close(dx, _np(y.double() @ w[-1].double()), _np(y.double().abs() @ w[-1].double().abs()), N)
+    del w
+    dw = g.grad_w(y, x, off)
+    _close(dw[-1], _np(y.double().t() @ x.double()), _np(y.double().abs().t() @ x.double().abs()), R)
+    assert int(dw[:-1].view(torch.int16).count_nonzero()) == 0
+
+
 def test_autograd():
     g = _g()
     for dtype, out in ((torch.bfloat16, None), (torch.float16, torch.float32)):
@@ -231,6 +252,36 @@ def test_gradients_against_differences():
             (g.grad_w(c.cdy, c.cx, c.offsets, torch.float32), (c.cx, c.cw + dw), (c.cx, c.cw - dw), (c.cw + dw).double() - (c.cw - dw).double())):
         want = (got.double() * along).sum()
         assert abs(float(f(*plus) - f(*minus) - want)) <= 1e-4 * float((got.double() * along).abs().sum())
+
+
+def test_saved_operands_that_change():
+    """A backward that saved x, w or the offsets does not run on values written since."""
+    g = _g()
+    c = Case([9, 3], 64, 16, torch.bfloat16)
+    for which in range(3):
+        x, w, off = c.cx.clone().requires_grad_(), c.cw.clone().requires_grad_(), c.offsets.clone()
+        y = g.linear(x, w, off)
+        with torch.no_grad():
+            (x, w, off)[which].zero_()
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.sum().backward()
+
+
+def test_two_streams_at_once():
+    g = _g()
+    a, b = Case([100, 30], 520, 392, torch.bfloat16), Case([7, 0, 200], 136, 1032, torch.float16)
+    want = [g.linear(c.cx, c.cw, c.offsets) for c in (a, b)] + [g.grad_w(c.cdy, c.cx, c.offsets) for c in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(5):
+        for c, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                got.append((c, g.linear(c.cx, c.cw, c.offsets), g.grad_w(c.cdy, c.cx, c.offsets)))
+    torch.cuda.synchronize()
+    for c, y, dw in got:
+        i = 0 if c is a else 1
+        assert torch.equal(y.nan_to_num(), want[i].nan_to_num()) and torch.equal(dw, want[2 + i])
 
 
 def test_repeatable_other_stream_and_graph():

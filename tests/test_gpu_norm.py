@@ -91,6 +91,43 @@ def test_strided_rows_at_any_element(dtype):
     assert torch.equal(y, norm.rms_norm(x.contiguous(), w.clone())[0])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_gradients_at_odd_addresses(dtype):
+    """h strided, dy and dh contiguous but one and three elements behind an aligned address."""
+    norm = _norm()
+    for T, H in ((9, 256), (5, 1000), (3, 4096)):
+        h, w = _rows(T, H, dtype, 1, pad=7), _weight(H, dtype, 2)
+        dy, dh = (torch.empty(T * H + k, dtype=dtype, device="cuda")[k:].view(T, H).copy_(_rows(T, H, dtype, 3 + k)) for k in (1, 3))
+        _, _, rstd = norm.rms_norm(h, w)
+        a = norm.backward(h, w, rstd, dy, dh)
+        b = norm.backward(h.contiguous(), w, rstd, dy.clone(), dh.clone())
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_rows_beyond_32_bits_of_bytes():
+    """x, h and y of more than 4 GiB: the last rows are the same rows alone."""
+    norm = _norm()
+    T, H = 270001, 8192
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    x.zero_()
+    x[-5:] = _rows(5, H, torch.bfloat16, 1)
+    x[0] = _rows(1, H, torch.bfloat16, 2)
+    w = _weight(H, torch.bfloat16, 3)
+    y, h, rstd = norm.rms_norm(x, w, x)
+    a, b, c = norm.rms_norm(x[-5:], w, x[-5:])
+    assert torch.equal(y[-5:], a) and torch.equal(h[-5:], b) and torch.equal(rstd[-5:], c) and torch.all(y[1] == 0)
+    codes, scales, _ = norm.rms_norm_mxfp8(x, w)
+    assert torch.equal(codes[-5:], norm.rms_norm_mxfp8(x[-5:], w)[0])
+    q, s = _mx().quantize(x)
+    assert torch.equal(q[-5:], _mx().quantize(x[-5:].contiguous())[0]) and torch.equal(s[-5:], _mx().quantize(x[-5:].contiguous())[1])
+    del y, codes, scales, q, s
+    dx, dg = norm.backward(h, w, rstd, h)
+    want = norm.backward(torch.cat([h[:1], h[-5:]]), w, torch.cat([rstd[:1], rstd[-5:]]), torch.cat([h[:1], h[-5:]]))
+    assert torch.equal(dx[-5:], want[0][1:])
+    # rows of zeros add nothing to dweight; the six others are summed in another order
+    assert bool(((dg.double() - want[1].double()).abs() <= 2.0 ** -7 * want[1].double().abs()).all())
+
+
 @pytest.mark.parametrize("T", [3000, 5003])
 def test_many_rows(T):
     _check(T, 96, torch.bfloat16, torch.bfloat16, residual=True, dh=True)

@@ -34,10 +34,9 @@ def quantize(x: torch.Tensor):
     _int32(K=K)
     if not x.is_cuda:
         _same_device([("x", x)])
-    dev = x.device
     codes = torch.empty_like(x, dtype=torch.uint8)
-    scales = torch.empty((*x.shape[:-1], K // 32), dtype=torch.uint8, device=dev)
-    _launch(dev.index, lib.tmoe_mxfp8_quantize, "tmoe_mxfp8_quantize", x.data_ptr(), _DTYPES[x.dtype], x.numel() // K, K,
+    scales = x.new_empty((*x.shape[:-1], K // 32), dtype=torch.uint8)
+    _launch(x.get_device(), lib.tmoe_mxfp8_quantize, "tmoe_mxfp8_quantize", x.data_ptr(), _DTYPES[x.dtype], x.numel() // K, K,
             codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
@@ -65,9 +64,8 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float32) -
         raise ValueError(f"dtype: {dtype}, expected one of {[str(d) for d in _DTYPES]}")
     if not _one_gpu(codes, scales):
         _same_device([("codes", codes), ("scales", scales)])
-    dev = codes.device
     x = torch.empty_like(codes, dtype=dtype)
-    _launch(dev.index, lib.tmoe_mxfp8_dequantize, "tmoe_mxfp8_dequantize", codes.data_ptr(), scales.data_ptr(),
+    _launch(codes.get_device(), lib.tmoe_mxfp8_dequantize, "tmoe_mxfp8_dequantize", codes.data_ptr(), scales.data_ptr(),
             x.numel() // K, K, _DTYPES[dtype], x.data_ptr())
     return x
 
@@ -88,9 +86,8 @@ def grouped_linear(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch
     if not _one_gpu(x_codes, x_scales, w_codes, w_scales, offsets):
         _same_device([("x codes", x_codes), ("x scales", x_scales), ("w codes", w_codes), ("w scales", w_scales),
                       ("offsets", offsets)])
-    dev = x_codes.device
-    y = torch.empty((R, N), dtype=out_dtype, device=dev)
-    _launch(dev.index, lib.tmoe_grouped_linear_mxfp8, "tmoe_grouped_linear_mxfp8",
+    y = x_codes.new_empty((R, N), dtype=out_dtype)
+    _launch(x_codes.get_device(), lib.tmoe_grouped_linear_mxfp8, "tmoe_grouped_linear_mxfp8",
             _config(E, K, N, torch.bfloat16, out_dtype, offsets.dtype), x_codes.data_ptr(), x_scales.data_ptr(),
             w_codes.data_ptr(), w_scales.data_ptr(), offsets.data_ptr(), R, y.data_ptr())
     return y

@@ -55,6 +55,13 @@ def _rows(t, name: str, shape=None, dtype=None) -> int:
 
 def _inputs(x, weight, residual, eps):
     """(configuration, strides) of inputs that the library can take."""
+    if isinstance(x, torch.Tensor) and isinstance(weight, torch.Tensor) and x.dim() == 2 and x.is_contiguous() and \
+            weight.is_contiguous() and weight.get_device() == x.get_device() >= 0:
+        T, H = x.shape                            # what most calls bring: one comparison
+        if weight.shape == (H,) and (weight.dtype is x.dtype or weight.dtype is torch.float32) and T < 2 ** 31 and \
+                H < 2 ** 31 and x.dtype in _DTYPES and (residual is None or (
+                    _fits(residual, x.shape, x.dtype) and residual.get_device() == x.get_device())):
+            return _config(H, x.dtype, weight.dtype, float(eps)), H, H
     stride = _rows(x, "x")
     H = x.shape[1]
     if not isinstance(weight, torch.Tensor) or weight.shape != (H,) or not weight.is_contiguous() or \
@@ -72,14 +79,14 @@ def _inputs(x, weight, residual, eps):
 
 def _rms_norm(x, weight, residual, eps):
     cfg, stride, res_stride = _inputs(x, weight, residual, eps)
-    T, dev = x.shape[0], x.device
+    T = x.shape[0]
     y = torch.empty_like(x, memory_format=_ROWS)
-    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    rstd = x.new_empty(T, dtype=torch.float32)
     h, ph, pr = x, None, None
     if residual is not None:
-        h = torch.empty_like(x, memory_format=_ROWS)
+        h = torch.empty_like(y)
         ph, pr = h.data_ptr(), residual.data_ptr()
-    _launch(dev.index, lib.tmoe_rms_norm, "tmoe_rms_norm", cfg, x.data_ptr(), stride, pr, res_stride, weight.data_ptr(), T,
+    _launch(x.get_device(), lib.tmoe_rms_norm, "tmoe_rms_norm", cfg, x.data_ptr(), stride, pr, res_stride, weight.data_ptr(), T,
             y.data_ptr(), ph, rstd.data_ptr())
     return y, h, rstd
 
@@ -91,7 +98,7 @@ def backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torc
     if _in_forward_mode():
         _refuse_duals(h=h, weight=weight, rstd=rstd, dy=dy, dh=dh)
     cfg, stride, _ = _inputs(h, weight, None, 0.0)
-    shape, dtype, dev = h.shape, h.dtype, h.device
+    shape, dtype = h.shape, h.dtype
     T = shape[0]
     if not _fits(rstd, (T,), torch.float32):
         _require(rstd, "rstd", (T,), (torch.float32,))
@@ -108,8 +115,8 @@ def backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torc
     dx = torch.empty_like(h, memory_format=_ROWS)
     dweight = torch.empty_like(weight)
     need = _scratch_bytes(cfg, T)
-    scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch(dev.index, lib.tmoe_rms_norm_backward, "tmoe_rms_norm_backward", cfg, h.data_ptr(), stride, weight.data_ptr(),
+    scratch = h.new_empty(need, dtype=torch.uint8)
+    _launch(h.get_device(), lib.tmoe_rms_norm_backward, "tmoe_rms_norm_backward", cfg, h.data_ptr(), stride, weight.data_ptr(),
             rstd.data_ptr(), dy.data_ptr(), pdh, T, dx.data_ptr(), dweight.data_ptr(), scratch.data_ptr(), need)
     return dx, dweight
 
@@ -139,7 +146,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     or fp32): h = x + residual (x itself without one), y = h / sqrt(mean(h^2) + eps) * weight."""
     if _in_forward_mode():
         _refuse_duals(x=x, weight=weight, residual=residual)
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, weight, residual)):
+    if torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(weight, "requires_grad", False)
+                                    or getattr(residual, "requires_grad", False)):
         out = _RmsNorm.apply(x, weight, residual, eps)
         return out if residual is not None else (out[0], x, out[1])
     return _rms_norm(x, weight, residual, eps)
@@ -150,15 +158,15 @@ def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     Forward only: tensors that require a gradient are refused."""
     _no_gradient(x=x, weight=weight, residual=residual)
     cfg, stride, res_stride = _inputs(x, weight, residual, eps)
-    (T, H), dev = x.shape, x.device
+    T, H = x.shape
     if H % 32:
         raise ValueError(f"x: rows of {H} values, expected a multiple of 32")
     codes = torch.empty_like(x, dtype=torch.uint8, memory_format=_ROWS)
-    scales = torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
+    scales = x.new_empty((T, H // 32), dtype=torch.uint8)
     h, ph, pr = x, None, None
     if residual is not None:
         h = torch.empty_like(x, memory_format=_ROWS)
         ph, pr = h.data_ptr(), residual.data_ptr()
-    _launch(dev.index, lib.tmoe_rms_norm_mxfp8, "tmoe_rms_norm_mxfp8", cfg, x.data_ptr(), stride, pr, res_stride,
+    _launch(x.get_device(), lib.tmoe_rms_norm_mxfp8, "tmoe_rms_norm_mxfp8", cfg, x.data_ptr(), stride, pr, res_stride,
             weight.data_ptr(), T, codes.data_ptr(), scales.data_ptr(), ph)
     return codes, scales, h
