@@ -45,6 +45,7 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 __device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 7) ^ ((r & 1) << 2); }
 
 constexpr int kRsrcFlags = 0x00027000;           // raw buffer, 32-bit data
+constexpr int kNontemporal = 2;                  // a load's nt bit
 constexpr int kPastEnd = static_cast<int>(0x80000000u);   // an offset outside every buffer
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int bytes) {
@@ -55,8 +56,13 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 
 // SCALES (MXFP8): 4 copies the scales of four slots at a time, 1 of one slot; 0: no copies (byte loads).
 // DEPTH: depth of a slot; 128 bytes, or less where both operands are KS.
-template <int KIND, int WT_, int WC_, int MT_, int NT_, int SLOTS_, int SCALES_ = 0, int DEPTH_ = KIND == kKindMx8 ? 128 : 64>
+// PAST: what does not stay in L2 (kResults, kWeights).
+enum { kResults = 1, kWeights = 2 };
+template <int KIND, int WT_, int WC_, int MT_, int NT_, int SLOTS_, int SCALES_ = 0, int DEPTH_ = KIND == kKindMx8 ? 128 : 64,
+          int PAST_ = kResults>
 struct GTile {
+  template <int P> using With = GTile<KIND, WT_, WC_, MT_, NT_, SLOTS_, SCALES_, DEPTH_, P>;
+  static constexpr int PAST = PAST_;
   static constexpr int SCALES = SCALES_;
   static constexpr int WT = WT_, WC = WC_, MT = MT_, NT = NT_, SLOTS = SLOTS_;
   static constexpr int ES = KIND == kKindMx8 ? 1 : 2;             // bytes a value
@@ -190,7 +196,7 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
   auto issue = [&](int place, int i, __amdgpu_buffer_rsrc_t rr, __amdgpu_buffer_rsrc_t cr) __attribute__((always_inline)) {
     if (i < C.N)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(cr, (__attribute__((address_space(3))) void*)(ring + place * S::kSlot + S::TR * S::DEPTH * S::ES + (wv + 4 * i) * 1024),
-                                               16, C.offset(islot, i), 0, 0, 0);
+                                               16, C.offset(islot, i), 0, 0, S::PAST & kWeights ? kNontemporal : 0);
     else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, (__attribute__((address_space(3))) void*)(ring + place * S::kSlot + (wv + 4 * (i - C.N)) * 1024),
                                                16, R.offset(islot, i - C.N), 0, 0, 0);
@@ -444,8 +450,11 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
       for (int i = 0; i < MB * 32 / RPI; ++i) {
         const int r = RPI * i + lane / LPR, row = 32 * ((m0 + r / 32) * S::WT + wt) + r % 32;
         const i4v v = *reinterpret_cast<const i4v*>(mine + r * PITCH + (lane % LPR) * 16);
-        if (row < t.nrows && c < a.cols)
-          *reinterpret_cast<i4v*>(y + (static_cast<long long>(t.row0 + row) * a.cols + c) * OS) = v;
+        if (row < t.nrows && c < a.cols) {
+          i4v* const to = reinterpret_cast<i4v*>(y + (static_cast<long long>(t.row0 + row) * a.cols + c) * OS);
+          if constexpr (S::PAST & kResults) __builtin_nontemporal_store(v, to);
+          else *to = v;
+        }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
@@ -524,7 +533,7 @@ __device__ __forceinline__ bool find_rows_tile(const GroupedArgs& a, int col_til
 // times the average come first (`popular` of them at most: that many cannot be more than E / kPopular), their tiles dealt to
 // the XCDs in turn; then the others in contiguous runs, so that an XCD's L2 holds what they share. In the order of the
 // experts, popular ones that come late keep their XCD busy alone (E = 96, K = N = 1024, popularity falling as 1 / rank^1.1,
-// 16384 and 65536 rows: 109 and 241 us, popular ones first 95 and 192).
+// 16384 and 65536 rows: 109 and 241 us, popular ones first 95 and 192; results through L2).
 constexpr int kPopular = 3;
 
 template <class S>
@@ -583,7 +592,7 @@ __global__ __launch_bounds__(256, kWavesPerSimd<S>) void k_grouped_rows(GroupedA
   if constexpr (S::MT == 4 && KIND != kKindMx8) {
     // A group's last tile, of at most half the rows, with half the fragments (E = 96, K = N = 1024, 16384 rows with uneven
     // popularity: linear 72 -> 69.5 us, grad_x 72 -> 65.5; MXFP8 leaves single fragments out).
-    using Half = GTile<KIND, S::WT, S::WC, 2, S::NT, S::SLOTS>;
+    using Half = GTile<KIND, S::WT, S::WC, 2, S::NT, S::SLOTS, 0, S::DEPTH, S::PAST>;
     if (t.nrows <= Half::TR) {
       grouped_body<KIND, false, CKS, Half, OUT>(a, t, lds);
       return;
@@ -599,6 +608,22 @@ __global__ __launch_bounds__(256, kWavesPerSimd<S>) void k_grouped_grad_w(Groupe
   if (find_weight_tile<S>(a, row_tiles, col_tiles, popular, t)) grouped_body<KIND, true, true, S, OUT>(a, t, lds);
 }
 
+// Fewer tiles than this leave CUs idle that smaller tiles would use.
+constexpr long long kFillsChip = 192;
+
+// Results go past L2, where they would push out the operands (us, past it and not, E = 96, K = N = 1024, 16384 rows of uneven
+// popularity: dW 66 - 79 and 95, grad_x 60 - 65 and 66 - 70, MXFP8 37 - 46 and 43 - 46, the first where operands are in the
+// memory-side cache; 8192 rows: dW 50 and 75; E = 8, K = 2048, N = 4096, 16384 rows: grad_x 275 and 287, MXFP8 157 - 177 and
+// 180; linear with the quantisation of its result behind it 282 and 291, E = 96, 65536 rows 197 and 193), but for dW of few rows
+// an expert that fits the memory-side cache: that is little else than stores (E = 96, K = N = 1024, 1 row 36.4 and 31.4, 21
+// rows 37.5 and 36.5, 43 rows 44 and 55; E = 128, K = 2560, N = 640, 419 MB, 9 rows 77 and 91).
+// 16-bit weights that about one row tile reads go past L2, where enough workgroups have work to hide that these loads take longer
+// (us, past it and not, E = 96, K = N = 1024: 16 tokens of 8 experts 32.4 and 34.8, grad_x 30.2 and 34.0; 64: 30.9 and 34.7; 2048
+// 67.7 and 71.0; one token, 64 workgroups, 14.2 and 11.2; E = 1, 16 rows, K = N = 4096, 32 workgroups, 50.6 and 33.6). MXFP8 weights
+// are half as large: from HBM the gain is 2 to 5 %, but where one layer's are still in the memory-side cache they lose a fifth
+// (256 tokens 28.5 and 29.6, and 27.6 and 24.0).
+constexpr long long kHidesLatency = 256;
+
 template <int KIND, bool CKS, class S, int OUT>
 bool launch_rows(const GroupedArgs& a, hipStream_t s) {
   const int ct = (a.cols + S::TC - 1) / S::TC;
@@ -606,7 +631,14 @@ bool launch_rows(const GroupedArgs& a, hipStream_t s) {
   const long long tiles = std::min<long long>(a.rows, a.experts + 2 + a.rows / S::TR);
   const long long g = (tiles * ct + 7) / 8 * 8;
   if (g > kMaxTiles) return false;
-  hipLaunchKernelGGL((k_grouped_rows<KIND, CKS, S, OUT>), dim3(static_cast<unsigned>(g)), dim3(256), 0, s, a, ct);
+  const dim3 grid(static_cast<unsigned>(g)), block(256);
+  if constexpr (KIND != kKindMx8) {
+    if (a.rows <= static_cast<long long>(S::TR) * a.experts && static_cast<long long>(std::min(a.rows, a.experts)) * ct >= kHidesLatency) {
+      hipLaunchKernelGGL((k_grouped_rows<KIND, CKS, typename S::template With<kResults | kWeights>, OUT>), grid, block, 0, s, a, ct);
+      return true;
+    }
+  }
+  hipLaunchKernelGGL((k_grouped_rows<KIND, CKS, S, OUT>), grid, block, 0, s, a, ct);
   return true;
 }
 
@@ -626,9 +658,6 @@ template <int KIND, int SCALES = 0> using Few = GTile<KIND, 1, 4, 1, 1, 2, SCALE
 template <int KIND, int SCALES = 0> using Mid = GTile<KIND, 2, 2, 2, 2, 2, SCALES>;
 template <int KIND, int SCALES = 0> using Big = GTile<KIND, 2, 2, 4, 4, 2, SCALES>;
 template <int KIND> using Flat = GTile<KIND, 2, 2, 2, 2, 2, 0, 32>;   // 128 x 128, slots of 32 (four)
-
-// Fewer tiles than this leave CUs idle that smaller tiles would use.
-constexpr long long kFillsChip = 192;
 
 // The tile of linear and grad_x (us; bf16, E = 96, K = N = 1024 unless said; rows an expert on average):
 //   up to 32 rows   32 x 128 (1: 30, 128 x 128 42; 5: 34 and 45; 21: 46 and 52; 32: 51 and 51; 43: 53 and 51)
@@ -658,7 +687,9 @@ bool launch_16bit(const GroupedArgs& a, int op, hipStream_t s) {
   if (op == kGroupedGradX) return launch_rows_by_size<KIND, true, OUT>(a, s);
   const long long tiles = static_cast<long long>((a.out_rows + 255) / 256) * ((a.cols + 255) / 256) * a.experts;
   if (a.rows >= 512LL * a.experts && tiles >= kFillsChip) return launch_grad_w<KIND, Big<KIND>, OUT>(a, s);
-  return launch_grad_w<KIND, Flat<KIND>, OUT>(a, s);
+  const long long bytes = static_cast<long long>(a.experts) * a.out_rows * a.cols * (OUT == TMOE_F32 ? 4 : 2);
+  if (a.rows > 32LL * a.experts || passes_caches(bytes)) return launch_grad_w<KIND, Flat<KIND>, OUT>(a, s);
+  return launch_grad_w<KIND, typename Flat<KIND>::template With<0>, OUT>(a, s);
 }
 
 }  // namespace

@@ -15,6 +15,10 @@
 
 namespace tmoe {
 
+// A pass over more bytes than the memory-side cache holds (256 MiB) finds none of them there, and leaves none for the next:
+// what it reads goes past the caches. Smaller passes lose by that (16384 rows of 1024 bf16, 134 MB, norm: 23.5 us and 22.6).
+inline bool passes_caches(long long bytes) { return bytes > 256LL << 20; }
+
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
