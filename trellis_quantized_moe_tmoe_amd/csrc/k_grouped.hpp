@@ -16,9 +16,9 @@
 // buffer loads that give zeros past the end: rows past the group's, columns past the last and depth past K all become
 // zeros in LDS and need no masks in the loop.
 //
-// Per slot there are four sub-steps; each multiplies fragments that were read from LDS during the one before. One barrier
-// a slot, in front of its last sub-step: by then every wavefront has read all of the slot, and the copies of the slot
-// that follows the ring go there.
+// Per slot there are two or four sub-steps; each multiplies fragments that were read from LDS during the one before. One barrier
+// a slot (256 x 256 tiles: two), in front of its last sub-step: by then every wavefront has read all of the slot, and the
+// copies of the slot that follows the ring go there.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -533,7 +533,7 @@ __device__ __forceinline__ bool find_rows_tile(const GroupedArgs& a, int col_til
 // times the average come first (`popular` of them at most: that many cannot be more than E / kPopular), their tiles dealt to
 // the XCDs in turn; then the others in contiguous runs, so that an XCD's L2 holds what they share. In the order of the
 // experts, popular ones that come late keep their XCD busy alone (E = 96, K = N = 1024, popularity falling as 1 / rank^1.1,
-// 16384 and 65536 rows: 109 and 241 us, popular ones first 95 and 192; results through L2).
+// 16384 and 65536 rows: 68 and 222 us, popular ones first 64.5 and 180; 4096 rows 41 and 45).
 constexpr int kPopular = 3;
 
 template <class S>
@@ -591,7 +591,7 @@ __global__ __launch_bounds__(256, kWavesPerSimd<S>) void k_grouped_rows(GroupedA
   if (!find_rows_tile<S>(a, col_tiles, t)) return;
   if constexpr (S::MT == 4 && KIND != kKindMx8) {
     // A group's last tile, of at most half the rows, with half the fragments (E = 96, K = N = 1024, 16384 rows with uneven
-    // popularity: linear 72 -> 69.5 us, grad_x 72 -> 65.5; MXFP8 leaves single fragments out).
+    // popularity: linear 68 -> 65 us, grad_x 64.5 -> 63; MXFP8 leaves single fragments out).
     using Half = GTile<KIND, S::WT, S::WC, 2, S::NT, S::SLOTS, 0, S::DEPTH, S::PAST>;
     if (t.nrows <= Half::TR) {
       grouped_body<KIND, false, CKS, Half, OUT>(a, t, lds);
@@ -645,7 +645,7 @@ bool launch_rows(const GroupedArgs& a, hipStream_t s) {
 template <int KIND, class S, int OUT>
 bool launch_grad_w(const GroupedArgs& a, hipStream_t s) {
   const int rt = (a.out_rows + S::TR - 1) / S::TR, ct = (a.cols + S::TC - 1) / S::TC;
-  const int popular = a.rows >= 32LL * a.experts ? (a.experts - 1) / kPopular : 0;
+  const int popular = a.rows >= 64LL * a.experts ? (a.experts - 1) / kPopular : 0;
   const long long each = static_cast<long long>(rt) * ct;
   const long long g = (each * popular + 7) / 8 * 8 + (each * a.experts + 7) / 8 * 8;
   if (g > kMaxTiles) return false;
@@ -660,17 +660,17 @@ template <int KIND, int SCALES = 0> using Big = GTile<KIND, 2, 2, 4, 4, 2, SCALE
 template <int KIND> using Flat = GTile<KIND, 2, 2, 2, 2, 2, 0, 32>;   // 128 x 128, slots of 32 (four)
 
 // The tile of linear and grad_x (us; bf16, E = 96, K = N = 1024 unless said; rows an expert on average):
-//   up to 32 rows   32 x 128 (1: 30, 128 x 128 42; 5: 34 and 45; 21: 46 and 52; 32: 51 and 51; 43: 53 and 51)
-//   up to 128       128 x 128 (85: 55, 256 x 256 60; 170: 76 and 70; 683: 207 and 164)
-//   more            256 x 256, where there are enough of them (E = 8, K = 2048, N = 4096, 256 rows: linear, 192 tiles, 56 and
-//                   128 x 128 78; grad_x, 96 tiles, 83 and 77; E = 1, 1024 rows, K = N = 4096, 72 tiles: 72 and 44)
-// MXFP8 has half the slots for the same depth, so what a tile costs before and behind them counts more: 256 x 256 from a depth of
-// 4096 on (E = 1, 4096 rows, K = N = 4096: 65 and 76; depth 2048, E = 8, N = 4096, 2048 rows: 190 and 184; 1024, E = 96, 683
-// rows: 145 and 134).
+//   up to 24 rows   32 x 128 (1: 28, 128 x 128 40; 5: 30 and 41.5; 21: 41 and 47.5; 32: 51.5 and 47; 43: 52.5 and 49)
+//   up to 128       128 x 128 (85: 53, 256 x 256 56.5; 170: 72.5 and 63.5; 683: 203 and 165)
+//   more            256 x 256, where there are enough of them (E = 8, K = 2048, N = 4096, 256 rows: linear, 192 tiles, 53 and
+//                   128 x 128 73; grad_x, 96 tiles, 81.5 and 75.5; E = 1, 1024 rows, K = N = 4096, 72 tiles: 70 and 42.5)
+// MXFP8: 32 x 128 up to 32 rows (32: 24 and 25; 43: 26 and 25). It has half the slots for the same depth, so what a tile costs
+// before and behind them counts more: 256 x 256 from a depth of 4096 on (E = 1, 4096 rows, K = N = 4096: 65.5 and 76; depth 2048,
+// E = 8, N = 4096, 2048 rows: 177 and 155; 1024, E = 96, 683 rows: 144 and 127).
 template <int KIND, bool CKS, int OUT, int SCALES = 0>
 bool launch_rows_by_size(const GroupedArgs& a, hipStream_t s) {
   const long long E = a.experts, R = a.rows;
-  if (R <= 32 * E) return launch_rows<KIND, CKS, Few<KIND, SCALES>, OUT>(a, s);
+  if (R <= (KIND == kKindMx8 ? 32 : 24) * E) return launch_rows<KIND, CKS, Few<KIND, SCALES>, OUT>(a, s);
   if constexpr (KIND != kKindMx8 || SCALES > 0) {   // byte loads of scales leave no registers for 256 x 256
     const long long tiles = (R / 256 + (E + 1) / 2) * ((a.cols + 255) / 256);
     if (R >= 128 * E && tiles >= kFillsChip && (KIND != kKindMx8 || a.depth >= 4096)) return launch_rows<KIND, CKS, Big<KIND, SCALES>, OUT>(a, s);
@@ -678,9 +678,9 @@ bool launch_rows_by_size(const GroupedArgs& a, hipStream_t s) {
   return launch_rows<KIND, CKS, Mid<KIND, SCALES>, OUT>(a, s);
 }
 
-// The tile of grad_w: 128 x 128 with short slots up to 512 rows an expert (E = 96, K = N = 1024: 1 row 31, 256 x 256 45; 21: 36
-// and 47; 170: 84 and 79; E = 8, 256 rows, K = 2048, N = 4096: 52 and 59), 256 x 256 beyond (683: 185 and 160; E = 8, 2048 rows,
-// K = 2048, N = 4096: 293 and 234), where there are enough of them.
+// The tile of grad_w: 128 x 128 with short slots up to 512 rows an expert (E = 96, K = N = 1024: 1 row 31, 256 x 256 44; 21: 36
+// and 48; 170: 66 and 76; E = 8, 256 rows, K = 2048, N = 4096: 49 and 58), 256 x 256 beyond (683: 204 and 188; E = 8, 2048 rows,
+// K = 2048, N = 4096: 280 and 221), where there are enough of them.
 template <int KIND, int OUT>
 bool launch_16bit(const GroupedArgs& a, int op, hipStream_t s) {
   if (op == kGroupedLinear) return launch_rows_by_size<KIND, false, OUT>(a, s);
