@@ -465,3 +465,30 @@ def test_a_served_layer_in_8_bits():
         xq, xs, nq, ns, o = (t.cpu().numpy() for t in (codes, scales, wq, ws, off))
         cut = np.concatenate([M.cut_bound(M.powers(xq, xs)[o[e]:o[e + 1]], M.powers(nq, ns)[e]) for e in range(E)])
         _close(y, *M.grouped(M.values(xq, xs), M.values(nq, ns), o), H, cut)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("sizes,K,N", [([7 * i % 37 for i in range(64)], 264, 520), ([7 * i % 37 for i in range(64)], 1000, 136),
+                                       ([11 * i % 199 for i in range(32)], 72, 1032), ([11 * i % 199 for i in range(32)], 1160, 40),
+                                       ([300, 0] + [150] * 38, 72, 1800), ([300, 0] + [150] * 38, 1800, 72)])
+def test_weights_that_are_read_once(sizes, K, N, dtype):
+    """Many experts of about one row tile each: 32, 128 and 256 rows."""
+    Case(sizes, K, N, dtype, 3, 40).all()
+    Case(sizes, K, N, dtype, 0, 0).linear(torch.float32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_weight_gradients_of_few_rows_beyond_the_caches(dtype):
+    """Few rows an expert, and more bytes of dw than the memory-side cache holds."""
+    say(f"[case] grad_w beyond the caches {dtype}")
+    E, N, K = 130, 1032, 1024
+    off, R = _offsets([0, 5] * (E // 2 - 1) + [3, 70], 2, 1)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x, dy = (torch.randn(R, n, generator=gen, device="cuda").to(dtype) for n in (K, N))
+    offsets = torch.tensor(off, dtype=torch.int32).cuda()
+    assert E * N * K * 2 > 256 << 20
+    dw = _g().grad_w(dy, x, offsets)
+    for e in (1, 65, E - 2, E - 1):
+        a, b = dy[off[e]:off[e + 1]].double().t(), x[off[e]:off[e + 1]].double()
+        _close(dw[e], _np(a @ b), _np(a.abs() @ b.abs()), off[e + 1] - off[e])
+    assert torch.all(dw[0:E - 2:2] == 0)

@@ -346,3 +346,34 @@ def test_quantize_leading_dimensions_and_no_rows():
     assert np.array_equal(codes.cpu().numpy(), M.quantize(x.double().numpy())[0])
     codes, scales = _mx().quantize(torch.zeros(0, 64, device="cuda"))
     assert codes.shape == (0, 64) and _mx().dequantize(codes, scales).shape == (0, 64)
+
+
+@pytest.mark.parametrize("T,H,dtype,wdtype,residual,pad", [(17003, 1001, torch.float32, torch.float32, True, 1),
+                                                          (4110, 8200, torch.bfloat16, torch.float32, True, 0),
+                                                          (350007, 257, torch.float16, torch.float16, True, 3)])
+def test_more_bytes_than_the_caches_hold(T, H, dtype, wdtype, residual, pad):
+    """Forward and backward beyond 256 MiB, with rows at any element."""
+    assert T * H * dtype.itemsize * 4 > 256 << 20
+    _check(T, H, dtype, wdtype, residual, residual, pad)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_mxfp8_of_more_bytes_than_the_caches_hold(dtype):
+    """The same codes, scales and values as of parts that the caches hold."""
+    say(f"[case] mxfp8 beyond the caches {dtype}")
+    norm, mx = _norm(), _mx()
+    H = 2080
+    T = (256 << 20) // (H * (dtype.itemsize + 1)) + 3
+    x, w = _rows(T, H, dtype, 7), _weight(H, dtype, 8)
+    half = T // 2
+    q, s = mx.quantize(x)
+    v = mx.dequantize(q, s, dtype)
+    y = norm.rms_norm_mxfp8(x, w, x)
+    for a, b in ((0, half), (half, half + 1000), (T - 1000, T)):
+        part = x[a:b].contiguous()
+        pq, ps = mx.quantize(part)
+        assert torch.equal(q[a:b], pq) and torch.equal(s[a:b], ps)
+        assert torch.equal(v[a:b], mx.dequantize(pq, ps, dtype))
+        small = part[:1000]
+        for got, want in zip(y, norm.rms_norm_mxfp8(small, w, small)):
+            assert torch.equal(got[a:a + 1000], want)
