@@ -7,8 +7,8 @@
 //
 // A row is held in registers by 64 to 1024 threads, vectors of 16 bytes of x a lane (its last vector may be short), so
 // nothing is read twice. Rows may start at any element: the vectors are loaded at the element's alignment. Passes over more
-// than the caches hold read past them (16384 rows of 4096 bf16: 80 us forward, 6.7 TB/s, and 97 backward, 5.5 TB/s, instead
-// of 98 and 111).
+// than the caches hold read past them (16384 rows of 4096 bf16: 80 us forward, 6.7 TB/s, and 89 backward, 6.1 TB/s, instead
+// of 98 and 119).
 #include <algorithm>
 
 #include "tmoe.h"
@@ -179,10 +179,13 @@ __global__ void k_rms_norm(NormArgs a) {
   }
 }
 
+// Wavefronts a SIMD (the compiler's registers allow no more, or spill).
+constexpr int grad_waves(int nv) { return nv == 1 ? 5 : 4; }
+
 // One pass over the rows, workgroup g of a.groups every groups-th batch of rows, the next row's loads ahead of this one's sum;
 // dweight's sums over its rows stay in registers, are joined over the workgroup's rows and leave as one row of partial sums.
-template <class D, class W, int NV, bool WIDE, bool PAST, int WAVES = NV == 1 ? 5 : 4>
-__global__ __launch_bounds__(WIDE ? 1024 : 512, WAVES) void k_rms_norm_grad(NormGradArgs a) {
+template <class D, class W, int NV, bool WIDE, bool PAST>
+__global__ __launch_bounds__(WIDE ? 1024 : 512, grad_waves(NV)) void k_rms_norm_grad(NormGradArgs a) {
   constexpr int V = D::V;
   typedef typename D::T T;
   __shared__ float sh[2][16];
@@ -285,12 +288,6 @@ NormShape grad_shape(int hidden, int dtype) {
   return n;
 }
 
-// Wavefronts a SIMD: with 80 registers instead of 96 a CU holds three rows of six to eight wavefronts, not two (16384 rows of
-// 4096 bf16: 111 us instead of 119; the others lose by it: 8192 rows of 8192 138 and 120, 2048 fp32 values a row 108 and 101).
-int grad_waves(const NormShape& n, int dtype) {
-  return n.nv > 1 ? 4 : dtype != TMOE_F32 && n.threads > 320 && n.threads <= 512 && n.rows == 1 ? 6 : 5;
-}
-
 template <class D, class W, bool MX, bool PAST>
 void launch_norm(const NormArgs& a, int dtype, hipStream_t s) {
   const NormShape n = norm_shape(a.hidden, dtype);
@@ -312,8 +309,6 @@ void launch_grad(const NormGradArgs& a, int dtype, hipStream_t s) {
   if (a.groups == 0) {
   } else if (n.threads == 64) {
     hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, false, PAST>), g, b, 0, s, a);
-  } else if (grad_waves(n, dtype) == 6) {
-    if constexpr (D::V == 8) hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, true, PAST, 6>), g, b, 0, s, a);
   } else if (n.nv == 1) {
     hipLaunchKernelGGL((k_rms_norm_grad<D, W, 1, true, PAST>), g, b, 0, s, a);
   } else if (n.nv == 2) {
@@ -347,7 +342,7 @@ NormShape norm_shape(int hidden, int dtype) {
 int norm_grad_groups(int tokens, int hidden, int dtype) {
   const NormShape n = grad_shape(hidden, dtype);
   const int waves = n.threads * n.rows / 64, batches = (tokens + n.rows - 1) / n.rows;
-  const int resident = 256 * std::clamp(4 * grad_waves(n, dtype) / waves, 1, 8);
+  const int resident = 256 * std::clamp(4 * grad_waves(n.nv) / waves, 1, 8);
   return std::max(1, std::min({batches, resident, std::max(256, batches / 4)}));
 }
 
