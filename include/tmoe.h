@@ -366,7 +366,7 @@ typedef struct {
 
 /* x, residual: [T] rows of H values, their strides elements from row to row (>= H); residual may be null, h is then
  * null too; weight: [H]; y, h: [T][H]; rstd: fp32 [T], r of every row, or null. Pointers aligned to their elements.
- * T <= 2^22; T = 0 launches nothing. One launch; deterministic. */
+ * T < 2^22; T = 0 launches nothing. One launch; deterministic. */
 tmoe_status tmoe_rms_norm(const tmoe_norm_config *cfg, const void *x, int64_t x_stride, const void *residual,
                           int64_t residual_stride, const void *weight, int32_t T, void *y, void *h, float *rstd,
                           void *stream);

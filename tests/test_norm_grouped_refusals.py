@@ -219,3 +219,13 @@ def test_reference_by_hand():
         assert abs((f(h, g + e) - f(h, g - e)) / 2e-5 - dg[j]) < 1e-7
     y, _ = M.grouped(np.eye(3), np.arange(8.0).reshape(2, 2, 2)[:, :, [0, 1, 1]], [1, 1, 3])
     assert np.array_equal(y, [[0, 0], [5, 7], [5, 7]])
+
+
+def test_norm_rows_that_a_launch_has_threads_for(N):
+    """A row of 16384 values takes 1024 threads, and a launch has fewer than 2^32."""
+    c, need = _norm_cfg(N, hidden=16384), ctypes.c_size_t()
+    T = 1 << 22
+    assert N.lib.tmoe_rms_norm(c, FAKE, 16384, None, 0, FAKE, T, FAKE, None, FAKE, None) == 2
+    assert N.lib.tmoe_rms_norm_mxfp8(c, FAKE, 16384, None, 0, FAKE, T, FAKE, FAKE, None, None) == 2
+    assert N.lib.tmoe_rms_norm_backward_scratch(c, T, ctypes.byref(need)) == 2
+    assert N.lib.tmoe_rms_norm_backward_scratch(c, T - 1, ctypes.byref(need)) == 0

@@ -15,7 +15,7 @@ using namespace tmoe;
 namespace {
 
 constexpr int kMaxHidden = 16384;
-constexpr int kMaxTokens = 1 << 22;              // a row has up to 1024 threads, a launch fewer than 2^32
+constexpr int kMaxTokens = (1 << 22) - 1;        // a row has up to 1024 threads, a launch fewer than 2^32
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
