@@ -412,7 +412,7 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
     }
   }
 
-      // Results leave through the wavefront's own part of LDS, MB by NC fragments at a time, so that a store covers whole lines of
+  // Results leave through the wavefront's own part of LDS, MB by NC fragments at a time, so that a store covers whole lines of
   // a row.
   constexpr int OS = OUT == TMOE_F32 ? 4 : 2, EPL = 16 / OS;
   constexpr int NC = 4 * 32 * (32 * NT * OS + 16) > S::kLds ? NT / 2 : NT, PITCH = 32 * NC * OS + 16;
@@ -617,6 +617,7 @@ constexpr long long kFillsChip = 192;
 // 180; linear with the quantisation of its result behind it 282 and 291, E = 96, 65536 rows 197 and 193), but for dW of few rows
 // an expert that fits the memory-side cache: that is little else than stores (E = 96, K = N = 1024, 1 row 36.4 and 31.4, 21
 // rows 37.5 and 36.5, 43 rows 44 and 55; E = 128, K = 2560, N = 640, 419 MB, 9 rows 77 and 91).
+//
 // 16-bit weights that about one row tile reads go past L2, where enough workgroups have work to hide that these loads take longer
 // (us, past it and not, E = 96, K = N = 1024: 16 tokens of 8 experts 32.4 and 34.8, grad_x 30.2 and 34.0; 64: 30.9 and 34.7; 2048
 // 67.7 and 71.0; one token, 64 workgroups, 14.2 and 11.2; E = 1, 16 rows, K = N = 4096, 32 workgroups, 50.6 and 33.6). MXFP8 weights
