@@ -16,7 +16,8 @@ SOURCES = ["k_route_map.hip", "k_rowops.hip", "k_trellis_gemm.hip", "k_small_arm
            "k_grouped_mxfp8.hip", "tmoe_host.cpp", "tmoe_router_host.cpp", "tmoe_mxfp4_host.cpp", "tmoe_norm_host.cpp",
            "tmoe_grouped_host.cpp"]
 HEADERS = ["tmoe_device.hpp", "tmoe_hadamard.hpp", "tmoe_internal.hpp", "tmoe_rowbody.hpp", "tmoe_routemap.hpp",
-           "tmoe_router.hpp", "tmoe_mxfp4.hpp", "tmoe_mxfp8.hpp", "tmoe_norm.hpp", "tmoe_grouped.hpp", "k_grouped.hpp"]
+           "tmoe_router.hpp", "tmoe_mxfp4.hpp", "tmoe_mxfp8.hpp", "tmoe_norm.hpp", "tmoe_grouped.hpp", "tmoe_grouped_scales.hpp",
+           "k_grouped.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

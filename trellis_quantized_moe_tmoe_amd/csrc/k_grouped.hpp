@@ -26,6 +26,7 @@
 #include "tmoe.h"
 #include "tmoe_device.hpp"
 #include "tmoe_grouped.hpp"
+#include "tmoe_grouped_scales.hpp"
 
 namespace tmoe {
 
@@ -205,12 +206,11 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
   // the last ones of a row starting where they end with it (one slot at a time, 4 bytes a row, asks L2 for as many lines as
   // the codes: 535 us instead of 519 at 8192 x 8192 x 8192).
   const int nblk = MX ? a.depth / 32 : 0;
-  auto scales_from = [&](int slot) __attribute__((always_inline)) { return S::SCALES == 4 ? min(4 * slot, nblk - 16) : 4 * slot; };
   auto issue_scales = [&]() __attribute__((always_inline)) {
     if constexpr (S::SCALES > 0) {
       if (S::SCALES > 1 && islot % S::SCALES != 0) return;
       constexpr int CN = S::TC / 64, ALL = S::kScaleRows / 64;
-      const int from = scales_from(islot);
+      const int from = S::SCALES == 4 ? scales_from(islot, nblk) : 4 * islot;
 #pragma unroll
       for (int i = 0; i < S::SPW; ++i) {
         const int j = min(wv + 4 * i, ALL - 1);
@@ -227,7 +227,7 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
   auto scales_at = [&](int slot, int row) __attribute__((always_inline)) {
     typedef __attribute__((address_space(3))) int lds_i;
     return *(lds_i*)(ring + S::kRing + slot / max(S::SCALES, 1) % 2 * S::kScaleBuffer + 4 * S::SCALES * row +
-                     (S::SCALES == 4 ? 4 * slot - scales_from(slot / 4 * 4) : 0));
+                     (S::SCALES == 4 ? scale_place(slot, nblk) : 0));
   };
 
   struct Frags {
