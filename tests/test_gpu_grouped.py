@@ -492,3 +492,38 @@ def test_weight_gradients_of_few_rows_beyond_the_caches(dtype):
         a, b = dy[off[e]:off[e + 1]].double().t(), x[off[e]:off[e + 1]].double()
         _close(dw[e], _np(a @ b), _np(a.abs() @ b.abs()), off[e + 1] - off[e])
     assert torch.all(dw[0:E - 2:2] == 0)
+
+
+def _spread_sizes(E, sizes, rest):
+    """E groups: `sizes` by index, `rest` in the others."""
+    return [sizes.get(e, rest) for e in range(E)]
+
+
+# sizes, how many of the experts have more than three times the average, K, N
+POPULAR = [([65] * 9, 0, 136, 72),
+           ([2700] + [0] * 40, 1, 136, 72),
+           ([0] * 40 + [2700], 1, 136, 72),
+           (_spread_sizes(33, {e: 220 for e in range(0, 30, 3)}, 0), 10, 136, 72),         # as many as there can be: (E - 1) / 3
+           (_spread_sizes(33, {e: 220 for e in range(23, 33)}, 0), 10, 40, 264),
+           (_spread_sizes(136, {63: 2100, 64: 2107, 130: 2200}, 20), 3, 136, 72),          # on both sides of 64, and in the third 64
+           (_spread_sizes(512, {0: 5000, 447: 5003, 448: 4999, 450: 5000, 511: 5001}, 16), 5, 72, 136),
+           (_spread_sizes(200, {e: 350 for e in range(130, 196)}, 0), 66, 8, 24),          # as many as there can be, behind the second 64
+           ([100, 0, 2400, 60, 30], 1, 1544, 1800),                                        # 256 x 256 tiles
+           ([1700, 10, 0, 1750, 20, 100, 30], 2, 1544, 1800)]
+
+
+@pytest.mark.parametrize("sizes,popular,K,N", POPULAR)
+def test_popular_experts_come_first_and_are_all_written(sizes, popular, K, N):
+    """grad_w looks popular experts up from 64 rows an expert on; every value of a result that held NaN is written."""
+    from trellis_quantized_moe_tmoe_amd import native as n
+    c = Case(sizes, K, N, torch.bfloat16)
+    E, R = len(sizes), c.R
+    assert R >= 64 * E and sum(s * E > 3 * R for s in sizes) == popular <= (E - 1) // 3
+    if K > 1024:
+        assert R >= 512 * E and -(-K // 256) * -(-N // 256) * E >= 192
+    dw = torch.full((E, N, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    cfg = ctypes.byref(n.GroupedConfig(E, K, N, n.BF16, n.BF16, n.IDS_I32))
+    assert n.lib.tmoe_grouped_grad_w(cfg, c.cdy.data_ptr(), c.cx.data_ptr(), c.offsets.data_ptr(), R, dw.data_ptr(),
+                                     torch.cuda.current_stream().cuda_stream) == 0
+    _close(dw, *M.grouped_grad_w(c.ndy, c.nx, c.off), np.diff(c.off)[:, None, None])
+    assert torch.all(dw[np.diff(c.off) == 0] == 0)
