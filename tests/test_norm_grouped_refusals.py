@@ -229,3 +229,19 @@ def test_norm_rows_that_a_launch_has_threads_for(N):
     assert N.lib.tmoe_rms_norm_mxfp8(c, FAKE, 16384, None, 0, FAKE, T, FAKE, FAKE, None, None) == 2
     assert N.lib.tmoe_rms_norm_backward_scratch(c, T, ctypes.byref(need)) == 2
     assert N.lib.tmoe_rms_norm_backward_scratch(c, T - 1, ctypes.byref(need)) == 0
+
+
+def test_quantising_a_leaf_that_wants_a_gradient():
+    """Only a parameter may be quantised as it is: any other tensor's gradient would get lost without a word."""
+    from trellis_quantized_moe_tmoe_amd import mxfp8
+    x = torch.zeros(4, 64, requires_grad=True)    # an input that the caller differentiates: a leaf
+    with pytest.raises(ValueError, match="x: requires a gradient"):
+        mxfp8.quantize(x)
+    for fine in (lambda: mxfp8.quantize(torch.nn.Parameter(torch.zeros(4, 64))), lambda: mxfp8.quantize(x.detach())):
+        with pytest.raises(ValueError, match="GPU device"):
+            fine()
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU device"):
+        mxfp8.quantize(x)
+    p = torch.nn.Parameter(torch.zeros(4, 64))
+    with forward_ad.dual_level(), torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):
+        mxfp8.quantize(forward_ad.make_dual(p, torch.ones(4, 64)))

@@ -4,8 +4,8 @@ Thin wrappers of tmoe_mxfp8_quantize, tmoe_mxfp8_dequantize and tmoe_grouped_lin
 and the formulas). Codes and scales are uint8 tensors [..., K] and [..., K/32]; weights are rows of output features,
 quantised along their input features: `mxfp8.quantize(w)` with w [E, N, K]. `norm.rms_norm_mxfp8` gives rows in this form.
 
-Forward only: no call here has a backward. Activations that require a gradient are refused (detach them, or call under
-torch.no_grad()); a leaf parameter can be quantised as it is."""
+Forward only: no call here has a backward. Tensors that require a gradient are refused (detach them, or call under
+torch.no_grad()), leaves among them; only a torch.nn.Parameter can be quantised as it is."""
 from __future__ import annotations
 
 import torch
@@ -22,7 +22,7 @@ def quantize(x: torch.Tensor):
     """(codes uint8 [..., K], scales uint8 [..., K/32]) of fp32, bf16 or fp16 values [..., K], K a multiple of 32."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x: expected a tensor [..., K]")
-    if x.grad_fn is not None:                     # a parameter itself may be quantised: nothing lies behind it
+    if x.requires_grad and not (x.is_leaf and isinstance(x, torch.nn.Parameter)):   # a parameter, as a program loads it
         _no_gradient(x=x)
     elif _in_forward_mode():
         _refuse_duals(x=x)
