@@ -356,7 +356,9 @@ tmoe_status tmoe_forward_mxfp4(tmoe_mxfp4_plan_t plan, const void *x_bf16, const
  *   dx = dh + r (g dy - h r^2 mean(g dy h))       the gradient of x and of the residual alike
  *   dg = sum over rows of dy h r
  * Sums are held in fp32; every output is rounded once. A row whose squares sum past fp32's largest value gives y = 0
- * (and NaN where it holds an infinity), one with a NaN gives NaN. Outputs must not overlap inputs. */
+ * (and NaN where it holds an infinity), one with a NaN gives NaN. Squares below fp32's smallest numbers count (with eps
+ * 0, or as small); r itself passes fp32's largest value, and is infinite, where sqrt(mean(h^2) + eps) is below 2^-128, and
+ * without eps a row of zeros is 0 / 0: gradients of such rows, and dg with them, are NaN. Outputs must not overlap inputs. */
 typedef struct {
   int32_t hidden;              /* H: 1..16384; MXFP8 output: a multiple of 32                    */
   int32_t dtype;               /* of x, residual, h, y and their gradients: TMOE_F32, BF16, F16  */

@@ -377,3 +377,47 @@ def test_mxfp8_of_more_bytes_than_the_caches_hold(dtype):
         small = part[:1000]
         for got, want in zip(y, norm.rms_norm_mxfp8(small, w, small)):
             assert torch.equal(got[a:a + 1000], want)
+
+
+@pytest.mark.parametrize("T,H", [(3, 40), (5, 1000), (2, 2049), (3, 4096), (2, 16384)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-33])
+def test_rows_whose_squares_are_too_small_for_fp32(T, H, dtype, eps):
+    """Squares below fp32's smallest numbers, beside no eps or one that is as small: the formula's values all the same."""
+    norm, eps = _norm(), float(np.float32(eps))
+    w = _weight(H, dtype, 2)
+    dy = _rows(T, H, dtype, 3).contiguous()
+    for p in (-45, -50, -63, -75, -90, -120):     # the root mean square; r = 2^-p at most
+        say(f"[case] norm {T}x{H} {dtype} eps {eps} of values near 2^{p}")
+        x = (_rows(T, H, torch.float32, 1).double() * 2.0 ** p).to(dtype)
+        x[0, 0] = 0.0
+        y, h, rstd = norm.rms_norm(x, w, eps=eps)
+        hn, g = _np(x), _np(w)
+        ref, u, r = M.norm(hn, g, eps)
+        assert np.all(np.abs(_np(rstd) - r[:, 0]) <= M.NORM_R * 1.001 * M.U * r[:, 0])
+        assert np.all(np.abs(_np(y) - ref) <= M.norm_bound(ref, HALF[dtype], TINY[dtype]))
+        if H % 32 == 0 and dtype == torch.float32:
+            assert torch.equal(torch.cat(norm.rms_norm_mxfp8(x, w, eps=eps)[:2], 1), torch.cat(_mx().quantize(y), 1))
+        if abs(p) > 100:                          # dx of order dy / 2^p passes the types' range
+            continue
+        dx, dg = norm.backward(h, w, rstd, dy)
+        args = (hn, g, eps, _np(dy), None)
+        wx, wg = M.norm_grad(*args)
+        bx, bg = M.norm_grad_bounds(*args, HALF[dtype], TINY[dtype], HALF[dtype], TINY[dtype])
+        assert np.all(np.abs(_np(dx) - wx) <= bx)
+        assert np.all(np.abs(_np(dg) - wg) <= bg)
+
+
+def test_rows_whose_rstd_passes_fp32():
+    """A root mean square below 2^-128: y is the formula's, r is infinite. Rows of zeros without eps: 0 / 0."""
+    norm = _norm()
+    x = _rows(3, 72, torch.float32, 1) * 2.0 ** -100 * 2.0 ** -35
+    x[1] = 0.0
+    w = _weight(72, torch.float32, 2)
+    y, _, rstd = norm.rms_norm(x, w, eps=0.0)
+    keep = [0, 2]
+    ref = M.norm(_np(x)[keep], _np(w), 0.0)[0]
+    assert np.all(np.abs(_np(y)[keep] - ref) <= M.norm_bound(ref, HALF[torch.float32], TINY[torch.float32]))
+    assert torch.isinf(rstd).all() and torch.isnan(y[1]).all()
+    x = torch.zeros(2, 72, dtype=torch.float16, device="cuda")
+    assert torch.isnan(norm.rms_norm(x, w, eps=0.0)[0]).all() and torch.all(norm.rms_norm(x, w)[0] == 0)

@@ -19,21 +19,25 @@ namespace tmoe {
 
 namespace {
 
+// SMALL: the type holds values whose squares fall below fp32's smallest numbers.
 struct F32 {
   typedef float T;
   static constexpr int V = 4;
+  static constexpr bool SMALL = true;
   static __device__ __forceinline__ float get(float v) { return v; }
   static __device__ __forceinline__ float put(float v) { return v; }
 };
 struct BF16 {
   typedef uint16_t T;
   static constexpr int V = 8;
+  static constexpr bool SMALL = true;
   static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
   static __device__ __forceinline__ uint16_t put(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
 };
 struct F16 {
   typedef uint16_t T;
   static constexpr int V = 8;
+  static constexpr bool SMALL = false;
   static __device__ __forceinline__ float get(uint16_t v) { return static_cast<float>(__builtin_bit_cast(_Float16, v)); }
   static __device__ __forceinline__ uint16_t put(float v) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v)); }
 };
@@ -118,7 +122,7 @@ __device__ __forceinline__ float row_sum(float v, float* sh) {
 template <class D, class W, int NV, bool WIDE, bool MX, bool PAST>
 __global__ void k_rms_norm(NormArgs a) {
   constexpr int V = D::V;
-  __shared__ float sh[16];
+  __shared__ float sh[16], sh_small[16];
   const int H = a.hidden, tid = threadIdx.x, threads = blockDim.x;
   const int t = blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.tokens) return;                     // whole wavefronts; WIDE: the whole workgroup
@@ -147,8 +151,27 @@ __global__ void k_rms_norm(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) sum = fmaf(h[j][i], h[j][i], sum);
   sum = row_sum<WIDE>(sum, sh);
-  const float rstd = 1.0f / sqrtf(sum / static_cast<float>(H) + a.eps);
-  if (a.rstd && tid == 0) a.rstd[t] = rstd;
+  const float square = sum / static_cast<float>(H) + a.eps;
+  float rstd = 1.0f / sqrtf(square), up = 1.0f;
+  if constexpr (D::SMALL) {
+    // Squares below 2^-126 lose their bits and vanish below 2^-150. Beside 2^-100 that is nothing; a row with less, its eps
+    // included, is taken 2^100 times as large (exactly): its values lie below 2^-43 (H <= 2^14), so their squares sum to at most
+    // 2^114, and the smallest one's square is 2^-98.
+    if (square < 0x1p-100f) {                    // the same for the whole row
+      sum = 0.0f;
+      up = 0x1p100f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          h[j][i] *= up;
+          sum = fmaf(h[j][i], h[j][i], sum);
+        }
+      sum = row_sum<WIDE>(sum, sh_small);
+      rstd = 1.0f / sqrtf(sum / static_cast<float>(H) + a.eps * up * up);
+    }
+  }
+  if (a.rstd && tid == 0) a.rstd[t] = rstd * up;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int at = (j * threads + tid) * V;
