@@ -527,3 +527,41 @@ def test_popular_experts_come_first_and_are_all_written(sizes, popular, K, N):
                                      torch.cuda.current_stream().cuda_stream) == 0
     _close(dw, *M.grouped_grad_w(c.ndy, c.nx, c.off), np.diff(c.off)[:, None, None])
     assert torch.all(dw[np.diff(c.off) == 0] == 0)
+
+
+def test_operands_that_no_gradient_reads_are_not_saved():
+    """dx reads w and dW reads x: with one operand tracked the other's gradient is nobody's, so the tracked one may change, or go."""
+    g = _g()
+    c = Case([9, 0, 30], 64, 32, torch.bfloat16)
+    other = torch.randn(c.x.shape, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    x = c.cx.clone().requires_grad_()             # frozen experts
+    y = g.linear(x, c.cw, c.offsets)
+    with torch.no_grad():
+        x.copy_(other)
+    y.backward(c.cdy)
+    assert torch.equal(x.grad, g.grad_x(c.cdy, c.cw, c.offsets))
+    w = c.cw.clone().requires_grad_()             # an input that nothing lies behind
+    y = g.linear(c.cx, w, c.offsets)
+    with torch.no_grad():
+        w.zero_()
+    y.backward(c.cdy)
+    assert torch.equal(w.grad, g.grad_w(c.cdy, c.cx, c.offsets))
+    # what is read is still guarded
+    for x, w, change in ((c.cx.clone().requires_grad_(), c.cw.clone(), 1), (c.cx.clone(), c.cw.clone().requires_grad_(), 0),
+                         (c.cx.clone().requires_grad_(), c.cw.clone(), 2), (c.cx.clone(), c.cw.clone().requires_grad_(), 2)):
+        off = c.offsets.clone()
+        y = g.linear(x, w, off)
+        with torch.no_grad():
+            (x, w, off)[change].zero_()
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward(c.cdy)
+    # and its memory is given back
+    leaf, off = torch.zeros(1 << 20, 16, dtype=torch.bfloat16, device="cuda", requires_grad=True), torch.tensor([0, 1 << 20], device="cuda")
+    w = torch.ones(1, 8, 16, dtype=torch.bfloat16, device="cuda")
+    x = leaf + 1
+    y = g.linear(x, w, off)
+    before = torch.cuda.memory_allocated()
+    del x
+    assert torch.cuda.memory_allocated() <= before - (32 << 20)
+    y.sum().backward()
+    assert torch.all(leaf.grad == 8)

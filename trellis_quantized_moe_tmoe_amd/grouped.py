@@ -144,14 +144,16 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, offsets, out_dtype):
         y = _linear(x, w, offsets, out_dtype)
-        ctx.save_for_backward(x, w, offsets)
+        track_x, track_w = ctx.needs_input_grad[:2]
+        ctx.save_for_backward(x if track_w else None, w if track_x else None, offsets)   # dw reads x, dx reads w
+        ctx.dtype = x.dtype
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
-        dy = dy.to(x.dtype).contiguous()          # an fp32 gradient is rounded once: the products take x's type
+        dy = dy.to(ctx.dtype).contiguous()        # an fp32 gradient is rounded once: the products take x's type
         dx = grad_x(dy, w, offsets) if ctx.needs_input_grad[0] else None
         dw = grad_w(dy, x, offsets) if ctx.needs_input_grad[1] else None
         return dx, dw, None, None
