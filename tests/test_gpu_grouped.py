@@ -565,3 +565,16 @@ def test_operands_that_no_gradient_reads_are_not_saved():
     assert torch.cuda.memory_allocated() <= before - (32 << 20)
     y.sum().backward()
     assert torch.all(leaf.grad == 8)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_gradient_that_arrives_at_an_odd_address(dtype):
+    """The gradient of a concatenation is a part of a larger one: contiguous, but not aligned to the products' 16 bytes."""
+    g = _g()
+    c = Case([20, 0, 45], 64, 24, dtype)
+    for lead in (1, 3, 4):
+        x, w = c.cx.clone().requires_grad_(), c.cw.clone().requires_grad_()
+        y = g.linear(x, w, c.offsets)
+        head = torch.zeros(lead, dtype=dtype, device="cuda")
+        torch.cat([head, y.flatten()]).backward(torch.cat([head, c.cdy.flatten()]))
+        assert torch.equal(x.grad, g.grad_x(c.cdy, c.cw, c.offsets)) and torch.equal(w.grad, g.grad_w(c.cdy, c.cx, c.offsets))

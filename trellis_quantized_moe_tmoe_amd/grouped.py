@@ -154,6 +154,8 @@ class _Linear(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.to(ctx.dtype).contiguous()        # an fp32 gradient is rounded once: the products take x's type
+        if dy.data_ptr() % 16:                    # a part of a larger gradient: the products copy from 16-byte addresses
+            dy = dy.clone()
         dx = grad_x(dy, w, offsets) if ctx.needs_input_grad[0] else None
         dw = grad_w(dy, x, offsets) if ctx.needs_input_grad[1] else None
         return dx, dw, None, None
