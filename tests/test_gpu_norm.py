@@ -421,3 +421,27 @@ def test_rows_whose_rstd_passes_fp32():
     assert torch.isinf(rstd).all() and torch.isnan(y[1]).all()
     x = torch.zeros(2, 72, dtype=torch.float16, device="cuda")
     assert torch.isnan(norm.rms_norm(x, w, eps=0.0)[0]).all() and torch.all(norm.rms_norm(x, w)[0] == 0)
+
+
+def test_a_weight_that_changes_before_its_own_gradient():
+    """dg does not read the weight: where it alone is trained it may be written before the backward; where dx is wanted it may not."""
+    norm = _norm()
+    x, r, dy = (_rows(9, 200, torch.float32, s).contiguous() for s in (1, 2, 3))
+    for res in (None, r):
+        w = _weight(200, torch.float32, 4).requires_grad_()
+        out = norm.rms_norm(x, w, res)
+        with torch.no_grad():
+            h, rstd = norm.rms_norm(x, w, res)[1:]
+            want = norm.backward(h, w, rstd, dy)[1]
+            w.zero_()
+        out[0].backward(dy)
+        assert torch.equal(w.grad, want)
+        w = _weight(200, torch.float32, 4).requires_grad_()
+        for tracked in ("x", "residual") if res is not None else ("x",):
+            a = dict(x=x, residual=res)
+            a[tracked] = a[tracked].clone().requires_grad_()
+            y = norm.rms_norm(weight=w, **a)[0]
+            with torch.no_grad():
+                w.mul_(2)
+            with pytest.raises(RuntimeError, match="inplace"):
+                y.backward(dy)

@@ -125,7 +125,12 @@ class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
         y, h, rstd = _rms_norm(x, weight, residual, eps)
-        ctx.save_for_backward(h, weight, rstd)
+        track_x, _, track_residual = ctx.needs_input_grad[:3]
+        if track_x or track_residual:
+            ctx.save_for_backward(h, weight, rstd)
+        else:                                     # dweight does not read the weight, which may change until then
+            ctx.save_for_backward(h, None, rstd)
+            ctx.weight = weight.detach()
         ctx.mark_non_differentiable(rstd)
         ctx.set_materialize_grads(False)
         return (y, rstd) if residual is None else (y, h, rstd)
@@ -134,6 +139,8 @@ class _RmsNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, *rest):
         h, weight, rstd = ctx.saved_tensors
+        if weight is None:
+            weight = ctx.weight                   # for the size and type; dx is nobody's
         dh = rest[0] if len(rest) == 2 else None
         if dy is None:                            # only h was used
             return dh, None, dh, None
