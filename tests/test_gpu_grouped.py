@@ -578,3 +578,16 @@ def test_a_gradient_that_arrives_at_an_odd_address(dtype):
         head = torch.zeros(lead, dtype=dtype, device="cuda")
         torch.cat([head, y.flatten()]).backward(torch.cat([head, c.cdy.flatten()]))
         assert torch.equal(x.grad, g.grad_x(c.cdy, c.cw, c.offsets)) and torch.equal(w.grad, g.grad_w(c.cdy, c.cx, c.offsets))
+
+
+def test_sizes_are_refused_before_outputs_are_allocated():
+    """Outputs that no card holds: the library's refusal, not the allocator's."""
+    from trellis_quantized_moe_tmoe_amd.native import TmoeError
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    off, R = torch.zeros(2, dtype=torch.int32, device="cuda"), 1 << 22
+    for call in (lambda: _g().linear(z(R, 8), z(1, 65544, 8), off), lambda: _g().grad_x(z(R, 8), z(1, 8, 65544), off),
+                 lambda: _g().grad_w(z(4, 65544), z(4, 65544), torch.zeros(513, dtype=torch.int32, device="cuda")),
+                 lambda: _mx().grouped_linear(u8(R, 32), u8(R, 1), u8(1, 65544, 32), u8(1, 65544, 1), off)):
+        with pytest.raises(TmoeError, match="UNSUPPORTED"):
+            call()

@@ -245,3 +245,13 @@ def test_quantising_a_leaf_that_wants_a_gradient():
     p = torch.nn.Parameter(torch.zeros(4, 64))
     with forward_ad.dual_level(), torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):
         mxfp8.quantize(forward_ad.make_dual(p, torch.ones(4, 64)))
+
+
+def test_grouped_configurations_are_refused_before_outputs_are_allocated(N):
+    from trellis_quantized_moe_tmoe_amd import grouped
+    for sizes in ((513, 64, 32), (4, 68, 32), (4, 64, 36), (4, 65544, 32), (4, 64, 65544)):
+        with pytest.raises(N.TmoeError, match="UNSUPPORTED"):
+            grouped._config(*sizes, torch.bfloat16, torch.bfloat16, torch.int32)
+    with pytest.raises(N.TmoeError, match="INVALID_ARG"):
+        grouped._config(4, 64, 0, torch.bfloat16, torch.bfloat16, torch.int32)
+    grouped._config(4, 64, 32, torch.bfloat16, torch.float32, torch.int64)

@@ -22,7 +22,7 @@ import torch
 
 from . import native
 from .layer import _in_forward_mode, _int32, _launch, _one_gpu, _refuse_duals, _same_device
-from .native import lib
+from .native import check, lib
 
 _DTYPES = {torch.bfloat16: native.BF16, torch.float16: native.F16, torch.float32: native.F32}
 _IDS = {torch.int32: native.IDS_I32, torch.int64: native.IDS_I64}
@@ -32,7 +32,10 @@ _BITS16 = (torch.bfloat16, torch.float16)
 @functools.lru_cache(maxsize=512)
 def _config(E: int, K: int, N: int, dtype, out_dtype, ids_dtype):
     _int32(E=E, K=K, N=N)
-    return ctypes.byref(native.GroupedConfig(E, K, N, _DTYPES[dtype], _DTYPES[out_dtype], _IDS[ids_dtype]))
+    cfg = ctypes.byref(native.GroupedConfig(E, K, N, _DTYPES[dtype], _DTYPES[out_dtype], _IDS[ids_dtype]))   # kept alive
+    # refused here, before a wrapper allocates outputs of these sizes: without rows nothing is launched
+    check(lib.tmoe_grouped_linear(cfg, None, None, None, 0, None, None), "grouped configuration")
+    return cfg
 
 
 def _check_offsets(offsets, E: Optional[int] = None) -> int:

@@ -86,8 +86,8 @@ def grouped_linear(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch
     if not _one_gpu(x_codes, x_scales, w_codes, w_scales, offsets):
         _same_device([("x codes", x_codes), ("x scales", x_scales), ("w codes", w_codes), ("w scales", w_scales),
                       ("offsets", offsets)])
+    cfg = _config(E, K, N, torch.bfloat16, out_dtype, offsets.dtype)
     y = x_codes.new_empty((R, N), dtype=out_dtype)
-    _launch(x_codes.get_device(), lib.tmoe_grouped_linear_mxfp8, "tmoe_grouped_linear_mxfp8",
-            _config(E, K, N, torch.bfloat16, out_dtype, offsets.dtype), x_codes.data_ptr(), x_scales.data_ptr(),
-            w_codes.data_ptr(), w_scales.data_ptr(), offsets.data_ptr(), R, y.data_ptr())
+    _launch(x_codes.get_device(), lib.tmoe_grouped_linear_mxfp8, "tmoe_grouped_linear_mxfp8", cfg, x_codes.data_ptr(),
+            x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), offsets.data_ptr(), R, y.data_ptr())
     return y
