@@ -45,6 +45,7 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 __device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 7) ^ ((r & 1) << 2); }
 
+constexpr int kRingSlots = 2;                    // the waits of the loop count on two; three and four gained nothing
 constexpr int kRsrcFlags = 0x00027000;           // raw buffer, 32-bit data
 constexpr int kNontemporal = 2;                  // a load's nt bit
 constexpr int kPastEnd = static_cast<int>(0x80000000u);   // an offset outside every buffer
@@ -55,28 +56,26 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, int byt
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// SCALES (MXFP8): 4 copies the scales of four slots at a time, 1 of one slot; 0: no copies (byte loads).
+// SCALES (MXFP8): scales are copied to LDS, those of four slots at a time; else they are loaded byte by byte.
 // DEPTH: depth of a slot; 128 bytes, or less where both operands are KS.
 // PAST: what does not stay in L2 (kResults, kWeights).
 enum { kResults = 1, kWeights = 2 };
-template <int KIND, int WT_, int WC_, int MT_, int NT_, int SLOTS_, int SCALES_ = 0, int DEPTH_ = KIND == kKindMx8 ? 128 : 64,
+template <int KIND, int WT_, int WC_, int MT_, int NT_, bool SCALES_ = false, int DEPTH_ = KIND == kKindMx8 ? 128 : 64,
           int PAST_ = kResults>
 struct GTile {
-  template <int P> using With = GTile<KIND, WT_, WC_, MT_, NT_, SLOTS_, SCALES_, DEPTH_, P>;
+  template <int P> using With = GTile<KIND, WT_, WC_, MT_, NT_, SCALES_, DEPTH_, P>;
   static constexpr int PAST = PAST_;
-  static constexpr int SCALES = SCALES_;
-  static constexpr int WT = WT_, WC = WC_, MT = MT_, NT = NT_, SLOTS = SLOTS_;
+  static constexpr bool SCALES = SCALES_;
+  static constexpr int WT = WT_, WC = WC_, MT = MT_, NT = NT_;
   static constexpr int ES = KIND == kKindMx8 ? 1 : 2;             // bytes a value
   static constexpr int DEPTH = DEPTH_;
   static constexpr int TR = 32 * MT * WT, TC = 32 * NT * WC;
   static constexpr int kSlot = (TR + TC) * DEPTH * ES;
   static constexpr int kScaleRows = SCALES ? TC + (TR + 63) / 64 * 64 : 0;
-  static constexpr int kScaleBuffer = 4 * SCALES * kScaleRows;    // one of two
-  static constexpr int kRing = SLOTS * kSlot;
+  static constexpr int kScaleBuffer = 16 * kScaleRows;            // one of two
+  static constexpr int kRing = kRingSlots * kSlot;
   static constexpr int kLds = kRing + 2 * kScaleBuffer;
   static constexpr int SPW = (kScaleRows / 64 + 3) / 4;           // scale copies of a wavefront
-  static constexpr int COPIES = kSlot / 4096;                     // copies a wavefront issues a slot
-  static_assert(SLOTS == 2 || !SCALES, "two buffers of scales");
   static_assert(WT * WC == 4, "four wavefronts");
 };
 
@@ -202,15 +201,15 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, (__attribute__((address_space(3))) void*)(ring + place * S::kSlot + (wv + 4 * (i - C.N)) * 1024),
                                                16, R.offset(islot, i - C.N), 0, 0, 0);
   };
-  // MXFP8 scales, columns first, then rows, in two buffers: with the first slot of every four (S::SCALES = 4) 16 bytes a row,
-  // the last ones of a row starting where they end with it (one slot at a time, 4 bytes a row, asks L2 for as many lines as
+  // MXFP8 scales, columns first, then rows, in two buffers: with the first slot of every four 16 bytes a row, the last ones of
+  // a row starting where they end with it (one slot at a time, 4 bytes a row, asks L2 for as many lines as
   // the codes: 535 us instead of 519 at 8192 x 8192 x 8192).
   const int nblk = MX ? a.depth / 32 : 0;
   auto issue_scales = [&]() __attribute__((always_inline)) {
-    if constexpr (S::SCALES > 0) {
-      if (S::SCALES > 1 && islot % S::SCALES != 0) return;
+    if constexpr (S::SCALES) {
+      if (islot % kScaleSlots != 0) return;
       constexpr int CN = S::TC / 64, ALL = S::kScaleRows / 64;
-      const int from = S::SCALES == 4 ? scales_from(islot, nblk) : 4 * islot;
+      const int from = scales_from(islot, nblk);
 #pragma unroll
       for (int i = 0; i < S::SPW; ++i) {
         const int j = min(wv + 4 * i, ALL - 1);
@@ -219,15 +218,14 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
         const uint8_t* p = col ? a.cs + (t.expert * a.cols + t.col0) * nblk : a.rs + static_cast<long long>(t.row0) * nblk;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rsrc(p + from, n * nblk - from),
-            (__attribute__((address_space(3))) void*)(ring + S::kRing + islot / S::SCALES % 2 * S::kScaleBuffer + 256 * S::SCALES * j),
-            4 * S::SCALES, row * nblk, 0, 0, 0);
+            (__attribute__((address_space(3))) void*)(ring + S::kRing + islot / kScaleSlots % 2 * S::kScaleBuffer + 1024 * j),
+            16, row * nblk, 0, 0, 0);
       }
     }
   };
   auto scales_at = [&](int slot, int row) __attribute__((always_inline)) {
     typedef __attribute__((address_space(3))) int lds_i;
-    return *(lds_i*)(ring + S::kRing + slot / max(S::SCALES, 1) % 2 * S::kScaleBuffer + 4 * S::SCALES * row +
-                     (S::SCALES == 4 ? scale_place(slot, nblk) : 0));
+    return *(lds_i*)(ring + S::kRing + slot / kScaleSlots % 2 * S::kScaleBuffer + 16 * row + scale_place(slot, nblk));
   };
 
   struct Frags {
@@ -280,7 +278,7 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
           if (s == 0) {
             const int row = 32 * (wc * NT + p) + r32;
             int w;
-            if constexpr (S::SCALES > 0) w = scales_at(slot, row);
+            if constexpr (S::SCALES) w = scales_at(slot, row);
             else w = scale_bytes(a.cs + (t.expert * a.cols + t.col0) * nblk, a.cols - t.col0, row, slot);
             f.cs[p] = w;
           }
@@ -300,7 +298,7 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
           if (s == 0) {
             const int row = 32 * (m * S::WT + wt) + r32;
             int w;
-            if constexpr (S::SCALES > 0) w = scales_at(slot, S::TC + row);
+            if constexpr (S::SCALES) w = scales_at(slot, S::TC + row);
             else w = scale_bytes(a.rs + static_cast<long long>(t.row0) * nblk, t.nrows, row, slot);
             f.rs[m] = w;
           }
@@ -331,30 +329,30 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
     for (int i = 0; i < CP; ++i) n += position(i) < q;
     return n;
   };
-  constexpr int kFirst = copies_below(P), kNewer = (S::SLOTS - 2) * S::COPIES + copies_below(kLanded);
+  constexpr int kFirst = copies_below(P), kNewer = copies_below(kLanded);
   static_assert(position(CP - 1) < P + kFree, "a slot's copies have gone out when the next one's start");
   // fragments in the order in which the matrix instructions want them
   auto piece = [](int p) { return p == 0 ? 0 : p == 1 ? NT : p <= NT ? p - 1 : p; };
   if (slots > 0) {
-    int place = 0, into = S::SLOTS - 1;          // the place that is read, the one that is written
+    int place = 0, into = kRingSlots - 1;        // the place that is read, the one that is written
     __amdgpu_buffer_rsrc_t rr, cr;
     Frags f[2];
 #pragma unroll
-    for (int d = 0; d < S::SLOTS; ++d) {
+    for (int d = 0; d < kRingSlots; ++d) {
       islot = d;
       issue_scales();
       rr = R.window(d), cr = C.window(d);
 #pragma unroll
-      for (int i = 0; i < (d == S::SLOTS - 1 ? kFirst : CP); ++i) issue(d, i, rr, cr);
+      for (int i = 0; i < (d == kRingSlots - 1 ? kFirst : CP); ++i) issue(d, i, rr, cr);
     }
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S::SLOTS - 2) * S::COPIES + kFirst) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kFirst) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int p = 0; p < MT + NT; ++p) read_piece(0, 0, 0, p, f[0]);
     const int fragments = (t.nrows + 32 * S::WT - 1) / (32 * S::WT);
     for (int slot = 0; slot < slots; ++slot) {
-      const int next = place + 1 == S::SLOTS ? 0 : place + 1;
+      const int next = place + 1 == kRingSlots ? 0 : place + 1;
       int rs[MT], cs[NT];
       if constexpr (MX) {
 #pragma unroll
@@ -374,7 +372,7 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& a, const Grouped
             else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kNewer) : "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            islot = slot + S::SLOTS;             // past the last one: zeros, which nobody reads
+            islot = slot + kRingSlots;           // past the last one: zeros, which nobody reads
             into = place;
             rr = R.window(islot), cr = C.window(islot);
           }
@@ -592,7 +590,7 @@ __global__ __launch_bounds__(256, kWavesPerSimd<S>) void k_grouped_rows(GroupedA
   if constexpr (S::MT == 4 && KIND != kKindMx8) {
     // A group's last tile, of at most half the rows, with half the fragments (E = 96, K = N = 1024, 16384 rows with uneven
     // popularity: linear 68 -> 65 us, grad_x 64.5 -> 63; MXFP8 leaves single fragments out).
-    using Half = GTile<KIND, S::WT, S::WC, 2, S::NT, S::SLOTS, 0, S::DEPTH, S::PAST>;
+    using Half = GTile<KIND, S::WT, S::WC, 2, S::NT, false, S::DEPTH, S::PAST>;
     if (t.nrows <= Half::TR) {
       grouped_body<KIND, false, CKS, Half, OUT>(a, t, lds);
       return;
@@ -655,10 +653,10 @@ bool launch_grad_w(const GroupedArgs& a, hipStream_t s) {
 }
 
 // Row tiles by columns: 32 x 128 (four workgroups a CU) while the weights' bytes count, 128 x 128 (two), 256 x 256 (one).
-template <int KIND, int SCALES = 0> using Few = GTile<KIND, 1, 4, 1, 1, 2, SCALES>;
-template <int KIND, int SCALES = 0> using Mid = GTile<KIND, 2, 2, 2, 2, 2, SCALES>;
-template <int KIND, int SCALES = 0> using Big = GTile<KIND, 2, 2, 4, 4, 2, SCALES>;
-template <int KIND> using Flat = GTile<KIND, 2, 2, 2, 2, 2, 0, 32>;   // 128 x 128, slots of 32 (four)
+template <int KIND, bool SCALES = false> using Few = GTile<KIND, 1, 4, 1, 1, SCALES>;
+template <int KIND, bool SCALES = false> using Mid = GTile<KIND, 2, 2, 2, 2, SCALES>;
+template <int KIND, bool SCALES = false> using Big = GTile<KIND, 2, 2, 4, 4, SCALES>;
+template <int KIND> using Flat = GTile<KIND, 2, 2, 2, 2, false, 32>;   // 128 x 128, slots of 32 (four)
 
 // The tile of linear and grad_x (us; bf16, E = 96, K = N = 1024 unless said; rows an expert on average):
 //   up to 24 rows   32 x 128 (1: 28, 128 x 128 40; 5: 30 and 41.5; 21: 41 and 47.5; 32: 51.5 and 47; 43: 52.5 and 49)
@@ -668,11 +666,11 @@ template <int KIND> using Flat = GTile<KIND, 2, 2, 2, 2, 2, 0, 32>;   // 128 x 1
 // MXFP8: 32 x 128 up to 32 rows (32: 24 and 25; 43: 26 and 25). It has half the slots for the same depth, so what a tile costs
 // before and behind them counts more: 256 x 256 from a depth of 4096 on (E = 1, 4096 rows, K = N = 4096: 65.5 and 76; depth 2048,
 // E = 8, N = 4096, 2048 rows: 177 and 155; 1024, E = 96, 683 rows: 144 and 127).
-template <int KIND, bool CKS, int OUT, int SCALES = 0>
+template <int KIND, bool CKS, int OUT, bool SCALES = false>
 bool launch_rows_by_size(const GroupedArgs& a, hipStream_t s) {
   const long long E = a.experts, R = a.rows;
   if (R <= (KIND == kKindMx8 ? 32 : 24) * E) return launch_rows<KIND, CKS, Few<KIND, SCALES>, OUT>(a, s);
-  if constexpr (KIND != kKindMx8 || SCALES > 0) {   // byte loads of scales leave no registers for 256 x 256
+  if constexpr (KIND != kKindMx8 || SCALES) {   // byte loads of scales leave no registers for 256 x 256
     const long long tiles = (R / 256 + (E + 1) / 2) * ((a.cols + 255) / 256);
     if (R >= 128 * E && tiles >= kFillsChip && (KIND != kKindMx8 || a.depth >= 4096)) return launch_rows<KIND, CKS, Big<KIND, SCALES>, OUT>(a, s);
   }
