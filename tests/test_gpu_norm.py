@@ -445,3 +445,17 @@ def test_a_weight_that_changes_before_its_own_gradient():
                 w.mul_(2)
             with pytest.raises(RuntimeError, match="inplace"):
                 y.backward(dy)
+
+
+def test_h_is_tracked_where_what_it_is_the_sum_of_is():
+    """h = x + residual does not depend on the weight: with that alone tracked nothing flows through h."""
+    norm = _norm()
+    x, r, dy = (_rows(9, 64, torch.float32, s).contiguous() for s in (1, 2, 3))
+    w = _weight(64, torch.float32, 4).requires_grad_()
+    y, h, rstd = norm.rms_norm(x, w, r)
+    assert y.requires_grad and not h.requires_grad and not rstd.requires_grad and torch.equal(h, x + r)
+    norm.rms_norm_mxfp8(h, w.detach())            # not refused
+    y.backward(dy)
+    assert torch.equal(w.grad, norm.backward(h, w.detach(), rstd, dy)[1])
+    for a, b in ((x.clone().requires_grad_(), r), (x, r.clone().requires_grad_())):
+        assert norm.rms_norm(a, w, b)[1].requires_grad and norm.rms_norm(a, w.detach(), b)[1].requires_grad

@@ -128,10 +128,11 @@ class _RmsNorm(torch.autograd.Function):
         track_x, _, track_residual = ctx.needs_input_grad[:3]
         if track_x or track_residual:
             ctx.save_for_backward(h, weight, rstd)
+            ctx.mark_non_differentiable(rstd)
         else:                                     # dweight does not read the weight, which may change until then
             ctx.save_for_backward(h, None, rstd)
             ctx.weight = weight.detach()
-        ctx.mark_non_differentiable(rstd)
+            ctx.mark_non_differentiable(*([rstd] if residual is None else [rstd, h]))
         ctx.set_materialize_grads(False)
         return (y, rstd) if residual is None else (y, h, rstd)
 
