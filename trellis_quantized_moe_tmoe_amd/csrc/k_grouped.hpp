@@ -652,7 +652,8 @@ bool launch_grad_w(const GroupedArgs& a, hipStream_t s) {
   return true;
 }
 
-// Row tiles by columns: 32 x 128 (four workgroups a CU) while the weights' bytes count, 128 x 128 (two), 256 x 256 (one).
+// Row tiles by columns: 32 x 128 (four workgroups a CU; three where MXFP8 scales are copied to LDS too) while the weights' bytes
+// count, 128 x 128 (two), 256 x 256 (one; with MXFP8 operands it spills 80 registers for fp32 results and 112 for bf16 ones).
 template <int KIND, bool SCALES = false> using Few = GTile<KIND, 1, 4, 1, 1, SCALES>;
 template <int KIND, bool SCALES = false> using Mid = GTile<KIND, 2, 2, 2, 2, SCALES>;
 template <int KIND, bool SCALES = false> using Big = GTile<KIND, 2, 2, 4, 4, SCALES>;

@@ -7,8 +7,8 @@
 //
 // A row is held in registers by 64 to 1024 threads, vectors of 16 bytes of x a lane (its last vector may be short), so
 // nothing is read twice. Rows may start at any element: the vectors are loaded at the element's alignment. Passes over more
-// than the caches hold read past them (16384 rows of 4096 bf16: 80 us forward, 6.7 TB/s, and 89 backward, 6.1 TB/s, instead
-// of 98 and 119).
+// than the caches hold read past them (16384 rows of 4096 bf16, residual, traced: forward 84 - 96 us, 5.6 - 6.4 TB/s, instead of
+// 89 - 98; backward 83 - 85, 6.4 TB/s, instead of 128).
 #include <algorithm>
 
 #include "tmoe.h"
@@ -202,7 +202,10 @@ __global__ void k_rms_norm(NormArgs a) {
   }
 }
 
-// Wavefronts a SIMD (the compiler's registers allow no more, or spill).
+// Wavefronts a SIMD. Rows of up to 8192 16-bit or 4096 fp32 values (one vector a lane) fit the registers of five, but for seven or
+// eight of fp16 rows of up to 512 values that the caches hold, which spill. Longer rows have a workgroup of up to 16 wavefronts, four
+// a SIMD, with 128 registers each: fp32 rows of up to 8192 values fit; beyond 8192 values 16-bit rows spill 5 - 133 registers (4096
+// x 12288 bf16, past the caches: 76 us, 5.3 TB/s) and fp32 rows 173 - 189 (247 us, 3.3 TB/s).
 constexpr int grad_waves(int nv) { return nv == 1 ? 5 : 4; }
 
 // One pass over the rows, workgroup g of a.groups every groups-th batch of rows, the next row's loads ahead of this one's sum;

@@ -12,7 +12,7 @@ using namespace tmoe;
 
 namespace {
 
-constexpr int kMaxExperts = 512;                 // two a thread in the kernels' scan
+constexpr int kMaxExperts = 512;                 // eight a lane in the kernels' search
 constexpr int kMaxDim = 1 << 16;
 constexpr int kMaxRows = 1 << 26;
 

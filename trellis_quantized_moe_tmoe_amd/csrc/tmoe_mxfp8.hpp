@@ -23,7 +23,7 @@ __device__ __forceinline__ uint32_t mxfp8_codes4(float a, float b, float c, floa
   return fp8x2_from_f32(a, b) | (fp8x2_from_f32(c, d) << 16);
 }
 
-// Largest of the values of 2 or 8 neighbouring lanes, and of 4 (mxfp4_quad_max): rows of 16 lanes, mirrored by halves.
+// Largest of the values of 8 neighbouring lanes: of each 4 (mxfp4_quad_max), then of the two, by mirroring the 8.
 __device__ __forceinline__ uint32_t mxfp8_oct_max(uint32_t v) {
   v = mxfp4_quad_max(v);
   const uint32_t o = __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);   // row_half_mirror
